@@ -96,6 +96,8 @@ typedef enum { QSA_F32 = 0, QSA_BF16 = 1, QSA_FP8_E4M3 = 2 } qsa_dtype_t;
 #define QSA_DEV_BAD_REQUEST 16u /* a request id outside [0, pt_rows) */
 #define QSA_DEV_TIMEOUT 32u   /* a bounded wait inside a kernel ran out (the
                                  kernel stopped early; its outputs are invalid) */
+#define QSA_DEV_NO_PAGE 64u   /* qsa_chunk_plan: the free list is shorter than the
+                                 pages the requests grow by */
 
 /* Before stage 1 -- the indexer projection (a reading fixed by this library:
  * "QSA in brief" names a learned indexer, not its layers).  y[t, n] =
@@ -408,6 +410,110 @@ QSA_API qsa_status_t qsa_dcp_expand(const int32_t* sel, const int32_t* n_sel, in
 QSA_API qsa_status_t qsa_dcp_merge_attn(const float* o_parts, const float* lse_parts, int R, int T, int Hq, int D,
                                         void* out, qsa_dtype_t out_dt, float* lse, qsa_stream_t stream);
 
+/* A dense chunk step over the paged cache.  The three calls below are what a
+ * serving step needs around the sparse path's stages: the tables and slots of
+ * its tokens, their rotary positions and cache write, and dense causal
+ * attention over everything cached (first chunks, sequences up to the
+ * sequence-length threshold, models or layers without an indexer).  They share
+ * the layouts above: pages of 64 tokens, [num_pages, 64, Hkv, D] caches,
+ * [pt_rows, pt_stride] page tables; batch entry b uses page-table row b.
+ * Limits: T <= 1,048,576 tokens, num_pages < 2^25, pt_stride <= 2^24. */
+
+/* Block tables and slot maps from the requests' lengths.  n_cached [B] tokens
+ * are in the cache, n_new [B] join in this step (B <= 8,192).  Outputs:
+ *   cu_new [B + 1]   tokens before each request (cu_new[B]: all tokens)
+ *   kv_len [B]       n_cached + n_new
+ *   q_req, q_pos [T] request and position of every new token, in batch order
+ *   slot [T]         its row in the cache seen as [num_pages * 64, Hkv, D]
+ *   n_taken [1]      pages taken from the free list
+ * Row b of page_table holds the pages of its cached tokens; the entries
+ * ceil(n_cached / 64) .. ceil(kv_len / 64) - 1 are filled from free_pages [n_free]
+ * in batch order (request 0's pages first) and every other entry stays as it
+ * is.  Rows of q_req, q_pos and slot behind the last token get -1 (a padded
+ * batch).  The inputs are not changed: a caller drops the first n_taken pages
+ * from its free list.
+ * Device checks: a negative length counts as 0; tokens past T are cut (cu_new
+ * and kv_len count the tokens kept); tokens past the page table's row have
+ * slot -1 (all three: QSA_DEV_ROW_RANGE); when the free list runs out, the
+ * entries get -1 and their tokens slot -1 (QSA_DEV_NO_PAGE); a page outside
+ * [0, num_pages) gives slot -1 (QSA_DEV_BAD_PAGE).
+ * The free list's pages must differ from each other and from the tables'.
+ * workspace: none (the query returns 0). */
+QSA_API size_t qsa_chunk_plan_workspace_size(int T, int B);
+QSA_API qsa_status_t qsa_chunk_plan(const int32_t* n_cached, const int32_t* n_new, int B, const int32_t* free_pages,
+                                    int n_free, int32_t* page_table, int pt_rows, int pt_stride, int num_pages, int T,
+                                    int32_t* cu_new, int32_t* kv_len, int32_t* q_req, int32_t* q_pos, int32_t* slot,
+                                    int32_t* n_taken, uint32_t* dev_status, qsa_stream_t stream);
+
+/* Rotary positions with one to three axes (time; time, height, width of
+ * images and video) on q and k, and the write of k and v into the cache.
+ * q [T, Hq, D], k and v [T, Hkv, D] in x_dt (F32 or BF16): rows q_stride /
+ * k_stride / v_stride values apart (multiples of 8), so that they may be
+ * slices of one projection's output; the heads of a row are contiguous.
+ * pos [n_axes, pos_stride] int32: position of token t on axis a at
+ * pos[a * pos_stride + t].  inv_freq [rot_dim / 2] F32.  For i < rot_dim / 2:
+ *   angle = pos[axis(i)][t] * inv_freq[i]
+ *   (a, b) -> rot_scale * (a cos - b sin, b cos + a sin)
+ * on (x[i], x[i + rot_dim/2]), or on (x[2i], x[2i+1]) when adjacent_pairs != 0.
+ * Values from rot_dim on are kept.  axis(i): with interleaved_axes == 0 the
+ * first sec0 frequencies take axis 0, the next sec1 axis 1, the last sec2 axis
+ * 2; otherwise axis 1 has i % 3 == 1 below 3 sec1, axis 2 has i % 3 == 2 below
+ * 3 sec2, and axis 0 the rest.  sec0 + sec1 + sec2 = rot_dim / 2; one axis:
+ * (rot_dim / 2, 0, 0).  Angles are reduced in 64 bits, so far positions keep
+ * their precision; the rotation is in FP32 and rounded once.
+ * q_out [T, Hq, D] in x_dt (it may be q itself when q is contiguous).  The
+ * rotated keys and the values go to rows slot[t] of k_pages / v_pages (kv_dt
+ * F32, BF16 or FP8_E4M3: code = value / scale to nearest even, values past 448
+ * saturate; the scales apply to FP8 only).  slot -1 marks padding: the
+ * token's q_out row and the cache stay as they are; any other slot outside
+ * [0, num_pages * 64) does the same and sets QSA_DEV_BAD_PAGE.  Slots must
+ * differ from each other.
+ * Supported: D 64, 128, 256; rot_dim a multiple of 16 up to D.
+ * workspace: none (the query returns 0). */
+QSA_API size_t qsa_rope_write_workspace_size(int T, int Hq, int Hkv, int D);
+QSA_API qsa_status_t qsa_rope_write(const void* q, int q_stride, const void* k, int k_stride, const void* v,
+                                    int v_stride, qsa_dtype_t x_dt, const int32_t* pos, int n_axes, int pos_stride,
+                                    int sec0, int sec1, int sec2, int interleaved_axes, int adjacent_pairs,
+                                    const float* inv_freq, int rot_dim, float rot_scale, const int32_t* slot, int T,
+                                    int Hq, int Hkv, int D, void* q_out, void* k_pages, void* v_pages,
+                                    qsa_dtype_t kv_dt, float k_scale, float v_scale, int num_pages,
+                                    uint32_t* dev_status, qsa_stream_t stream);
+
+/* Causal attention of every request's new tokens over all of its cached
+ * tokens (the new ones among them: their keys and values are already written).
+ * Request b's tokens are rows cu_new[b] .. cu_new[b+1] - 1 of q [T, Hq, D] and
+ * sit at positions kv_len[b] - n .. kv_len[b] - 1, n = cu_new[b+1] - cu_new[b];
+ * the token at p attends to tokens 0 .. p of page-table row b:
+ *   out[t,h,:] = sum_{j <= p} softmax(scale * q . K(j)) V(j)
+ *   lse[t,h]   = log sum_{j <= p} exp(scale * q . K(j))
+ * scale = sm_scale, or 1/sqrt(D) when sm_scale <= 0.  One token per request is
+ * decode, a few are drafts, many are a prompt's chunk; a batch may mix them.
+ * out has q's dtype; lse may be NULL.  A row without visible tokens (kv_len 0,
+ * or fewer cached than new tokens) gives zeros and -inf; rows from cu_new[B]
+ * on are left as they are.  Cache rows past kv_len are never used, whatever
+ * they hold, and neither is a token in a row's result that the row does not
+ * see (NaN or infinity included).
+ * Supported: D 64, 128, 256; Hq/Hkv <= 16; q F32 or BF16; caches F32, BF16 or
+ * FP8_E4M3 (value = code * scale); B <= 1,024.  A BF16 query on a BF16 or FP8
+ * cache runs on the tensor cores: logits, softmax and sums in FP32, the
+ * probabilities rounded to the type of the product with V (BF16 for a BF16
+ * cache, FP16 for an FP8 cache).  Other pairs run in FP32.
+ * Device checks: cu_new decreasing or outside [0, T], kv_len negative or past
+ * the page table's row: QSA_DEV_ROW_RANGE (tokens past the row are not
+ * attended); a page outside [0, num_pages): QSA_DEV_BAD_PAGE, its tokens are
+ * skipped.
+ * workspace: qsa_chunk_attn_workspace_size(...) bytes, 16-byte aligned, for the
+ * partial results of tiles that several CTAs share; every call writes what it
+ * reads there, so it needs no clearing, but calls that may overlap on the GPU
+ * need one each. */
+QSA_API size_t qsa_chunk_attn_workspace_size(int T, int B, int Hq, int Hkv, int D, qsa_dtype_t kv_dt);
+QSA_API qsa_status_t qsa_chunk_attn(const void* q, qsa_dtype_t q_dt, const void* k_pages, const void* v_pages,
+                                    qsa_dtype_t kv_dt, float k_scale, float v_scale, int num_pages,
+                                    const int32_t* page_table, int pt_rows, int pt_stride, const int32_t* cu_new,
+                                    const int32_t* kv_len, int B, int T, int Hq, int Hkv, int D, float sm_scale,
+                                    void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                    uint32_t* dev_status, qsa_stream_t stream);
+
 /* Device status query (the boundary's error channel for data the kernels
  * check on the device; see "Conventions" above).  Waits for `stream` to finish
  * the work queued so far, reads the caller's status word dev_status and
@@ -447,14 +553,16 @@ QSA_API qsa_status_t qsa_selftest_bounded_wait(uint32_t limit_us, uint32_t* dev_
 QSA_API const char* qsa_last_error_string(void);
 /* Static name of a status code. */
 QSA_API const char* qsa_status_name(qsa_status_t s);
-/* ABI version: bumped on any change of the entry points (2: the decode
+/* ABI version: bumped on any change of existing entry points (2: the decode
  * workspace query takes the KV dtype; 3: qsa_topk_expand; 4: the prefix_hist
  * argument of qsa_index_scores, qsa_topk_groups and qsa_topk_expand; 5: the
  * status codes QSA_ERR_DEVICE_INDEX / QSA_ERR_TIMEOUT, qsa_get_device_status
  * and a workspace query for every stage; 6: qsa_indexer_project and
  * qsa_compress_keys; 7: the sequence-sharded decode calls qsa_dcp_*; 8:
  * qsa_topk_groups_gvr; 9: qsa_seq_len_threshold and qsa_dense_select; 10:
- * qsa_selftest_bounded_wait; 11: qsa_sparse_attn_decode_sel). */
+ * qsa_selftest_bounded_wait; 11: qsa_sparse_attn_decode_sel).  Entry points
+ * added since, which change none of these: qsa_chunk_plan, qsa_rope_write and
+ * qsa_chunk_attn. */
 QSA_API int qsa_abi_version(void);
 
 #ifdef __cplusplus

@@ -1,0 +1,215 @@
+// chunk_common.cuh -- what the kernels of the chunk attention share: the
+// reading of a request's lengths, the cut of the work into tiles of query rows
+// and blocks of keys, and each CTA's share of it.
+#pragma once
+#include "qsa_internal.cuh"
+
+namespace qsa {
+
+constexpr int kChunkMaxReq = 1024;   // requests per chunk-attention call
+constexpr int kChunkMaxTiles = 1024; // query tiles per KV head of a call whose tiles are split over CTAs
+constexpr int kChunkMaxCtas = 148;   // CTAs that leave partials (one per SM of a B200)
+
+// A request as the device arrays give it.  `kv` is capped to the tokens a row
+// of the page table can address.
+struct ChunkReq {
+  int t0, n, p0, kv;  // first query token, tokens, position of the first one, cached tokens
+};
+__device__ __forceinline__ ChunkReq chunk_req(const ChunkArgs& a, int b, bool report) {
+  int lo = a.cu_new[b], hi = a.cu_new[b + 1], kv = a.kv_len[b];
+  const int cap = a.pt_stride * kPageTokens;
+  if (report && (lo < 0 || hi < lo || hi > a.T || kv < 0 || kv > cap)) flag(a.status, QSA_DEV_ROW_RANGE);
+  lo = min(max(lo, 0), a.T);
+  hi = min(max(hi, lo), a.T);
+  kv = max(kv, 0);
+  return ChunkReq{lo, hi - lo, kv - (hi - lo), min(kv, cap)};
+}
+
+// One CTA's piece of work: key blocks [blk_lo, blk_hi) of a tile of query
+// tokens and one KV head.
+struct ChunkItem {
+  int b, kvh, t0, ntok, p0, kv;
+  int blk_lo, blk_hi, nblk;
+  int part;      // -1: the whole tile; otherwise the slot its partial goes to
+  int n_parts;   // > 0: this piece holds the tile's first block, and so many pieces share the tile
+};
+
+// What a combine CTA needs to know of a tile that several CTAs share; entry c
+// is written by CTA c (n_parts = 0: none of CTA c's pieces opens a shared tile).
+// Partial slots: 2c + 1 for a piece that opens a tile CTA c does not finish,
+// 2c for a piece that starts inside a tile (CTA c's first).
+struct ChunkDesc {
+  int n_parts, t0, ntok, kvh;
+};
+
+// The cut of a call's work.  Query tiles hold TPT tokens of one request (all
+// query heads of one KV head); their keys fall into blocks of KT.  With few
+// tiles the linear (KV head, tile, block) space is divided evenly over the
+// CTAs, whatever the requests' lengths, and tiles that several CTAs share
+// are merged by the combine kernel.  With many tiles (four per CTA, or more
+// than the table holds) every tile is one CTA's; neighbouring CTAs then walk
+// the same keys at about the same time and share them in L2, and rounds run
+// in alternating order so that the causal tiles' growing lengths even out.
+struct ChunkSched {
+  int first[kChunkMaxReq + 1];    // query tiles before each request
+  int blk[kChunkMaxTiles + 1];    // shared tiles: key blocks before each query tile
+  int warp_sum[32];
+  int nq, shared_tiles;
+};
+
+// Exclusive prefix sum of v over the CTA's threads plus `carry`; returns this
+// thread's prefix and adds the total to carry.
+__device__ __forceinline__ int chunk_scan(int v, int* warp_sum, int& carry) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    const int s = warp_sum[w];
+    if (w < warp) before += s;
+    total += s;
+  }
+  __syncthreads();
+  const int out = carry + before + x - v;
+  carry += total;
+  return out;
+}
+
+__device__ __forceinline__ int chunk_tile_blocks(const ChunkReq& r, int tile, int TPT, int KT) {
+  const int last = min(r.n, (tile + 1) * TPT) - 1;          // the tile's last token
+  const int seen = min(r.p0 + last + 1, r.kv);              // keys it may see
+  return max(1, (seen + KT - 1) / KT);                      // an empty tile still writes its zeros
+}
+
+// The last index i of [0, n) with v[i] <= x (v ascending, v[0] <= x).
+__device__ __forceinline__ int chunk_find(const int* v, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (v[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Called by every thread of the CTA; the table is ready on return.
+__device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched& s, int TPT, int KT) {
+  int carry = 0;
+  for (int base = 0; base < a.B; base += blockDim.x) {
+    const int b = base + threadIdx.x;
+    int n = 0;
+    if (b < a.B) n = (chunk_req(a, b, blockIdx.x == 0).n + TPT - 1) / TPT;
+    const int before = chunk_scan(n, s.warp_sum, carry);
+    if (b < a.B) s.first[b] = before;
+  }
+  if (threadIdx.x == 0) {
+    s.first[a.B] = carry;
+    s.nq = carry;
+    s.shared_tiles = carry <= kChunkMaxTiles && (long long)carry * a.Hkv < 4ll * gridDim.x;
+  }
+  __syncthreads();
+  if (s.shared_tiles) {
+    const int nq = s.nq;
+    carry = 0;
+    for (int base = 0; base < nq; base += blockDim.x) {
+      const int q = base + threadIdx.x;
+      int n = 0;
+      if (q < nq) {
+        const int b = chunk_find(s.first, a.B, q);
+        n = chunk_tile_blocks(chunk_req(a, b, false), q - s.first[b], TPT, KT);
+      }
+      const int before = chunk_scan(n, s.warp_sum, carry);
+      if (q < nq) s.blk[q] = before;
+    }
+    if (threadIdx.x == 0) s.blk[nq] = carry;
+    __syncthreads();
+  }
+}
+
+// A CTA's walk over its pieces; every warp role runs its own copy.
+struct ChunkWalk {
+  long long u, u1, total;  // shared tiles: linear blocks; otherwise u counts rounds
+  int ctas;                // CTAs that have work
+
+  __device__ __forceinline__ void begin(const ChunkArgs& a, const ChunkSched& s) {
+    u = 0, u1 = 0, total = 0, ctas = gridDim.x;
+    if (s.shared_tiles) {
+      total = (long long)s.blk[s.nq] * a.Hkv;
+      if (total < ctas) ctas = (int)total;
+      if ((int)blockIdx.x < ctas) {
+        u = total * blockIdx.x / ctas;
+        u1 = total * (blockIdx.x + 1) / ctas;
+      }
+    }
+  }
+  __device__ __forceinline__ bool next(const ChunkArgs& a, const ChunkSched& s, int TPT, int KT, ChunkItem& it) {
+    int q;
+    if (s.shared_tiles) {
+      if (u >= u1) return false;
+      const int wq = s.blk[s.nq];
+      it.kvh = (int)(u / wq);
+      const int x = (int)(u - (long long)it.kvh * wq);
+      q = chunk_find(s.blk, s.nq, x);
+      it.blk_lo = x - s.blk[q];
+      it.nblk = s.blk[q + 1] - s.blk[q];
+      const long long left = u1 - u;
+      it.blk_hi = left < it.nblk - it.blk_lo ? it.blk_lo + (int)left : it.nblk;
+      it.part = -1, it.n_parts = 0;
+      if (it.blk_lo > 0) {
+        it.part = 2 * blockIdx.x;
+      } else if (it.blk_hi < it.nblk) {
+        it.part = 2 * blockIdx.x + 1;
+        const long long last = u + it.nblk - 1;                        // the tile's last linear block
+        const int owner = (int)(((last + 1) * ctas - 1) / total);      // the CTA whose share holds it
+        it.n_parts = owner - (int)blockIdx.x + 1;
+      }
+      u += it.blk_hi - it.blk_lo;
+    } else {
+      const long long idx = u * gridDim.x + ((u & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (u * gridDim.x >= (long long)s.nq * a.Hkv) return false;
+      ++u;
+      if (idx >= (long long)s.nq * a.Hkv) return false;  // only in the last round
+      it.kvh = (int)(idx / s.nq);
+      q = (int)(idx - (long long)it.kvh * s.nq);
+      it.part = -1, it.n_parts = 0;
+    }
+    it.b = chunk_find(s.first, a.B, q);
+    const ChunkReq r = chunk_req(a, it.b, false);
+    const int tile = q - s.first[it.b];
+    if (!s.shared_tiles) {
+      it.nblk = chunk_tile_blocks(r, tile, TPT, KT);
+      it.blk_lo = 0, it.blk_hi = it.nblk;
+    }
+    it.t0 = r.t0 + tile * TPT;
+    it.ntok = min(TPT, r.n - tile * TPT);
+    it.p0 = r.p0 + tile * TPT;
+    it.kv = r.kv;
+    return true;
+  }
+};
+
+// Partials of the split tiles: unnormalised outputs [slot][row][D], then
+// (running maximum in base 2, sum) [slot][row], then the tiles' descriptors.
+struct ChunkWs {
+  float* o;
+  float2* ml;
+  ChunkDesc* desc;
+};
+__host__ __device__ __forceinline__ size_t chunk_ws_bytes(int rows, int D) {
+  return (size_t)2 * kChunkMaxCtas * rows * (D * sizeof(float) + sizeof(float2)) + kChunkMaxCtas * sizeof(ChunkDesc);
+}
+__host__ __device__ __forceinline__ ChunkWs chunk_ws(void* ws, int rows, int D) {
+  ChunkWs w;
+  w.o = reinterpret_cast<float*>(ws);
+  w.ml = reinterpret_cast<float2*>(w.o + (size_t)2 * kChunkMaxCtas * rows * D);
+  w.desc = reinterpret_cast<ChunkDesc*>(w.ml + (size_t)2 * kChunkMaxCtas * rows);
+  return w;
+}
+
+}  // namespace qsa

@@ -36,6 +36,9 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
   } while (0)
 
 constexpr int kMaxGridY = 65535;
+constexpr int kMaxChunkTokens = 1 << 20;   // tokens of a plan, rotary or chunk-attention call
+constexpr int kMaxPages = (1 << 25) - 1;    // token rows of a cache stay below 2^31
+constexpr int kMaxRowPages = 1 << 24;       // tokens of a page-table row stay well below 2^31
 constexpr int kPageGroupsAbi = 16;   // groups per 64-token page
 
 qsa_status_t check_attn(const void* q, qsa_dtype_t q_dt, const void* k_pages, const void* v_pages,
@@ -132,10 +135,10 @@ qsa_status_t qsa_get_device_status(uint32_t* dev_status, uint32_t* bits_out, int
     return fail(QSA_ERR_TIMEOUT, "a bounded wait inside a kernel ran out (device status 0x%x)", bits);
   if (bits)
     return fail(QSA_ERR_DEVICE_INDEX,
-                "a kernel skipped out-of-range data on the device (device status 0x%x: %s%s%s%s%s)",
+                "a kernel skipped out-of-range data on the device (device status 0x%x: %s%s%s%s%s%s)",
                 bits, (bits & QSA_DEV_BAD_PAGE) ? "page " : "", (bits & QSA_DEV_BAD_TOKEN) ? "token " : "",
                 (bits & QSA_DEV_BAD_GROUP) ? "group " : "", (bits & QSA_DEV_ROW_RANGE) ? "row-range " : "",
-                (bits & QSA_DEV_BAD_REQUEST) ? "request" : "");
+                (bits & QSA_DEV_BAD_REQUEST) ? "request " : "", (bits & QSA_DEV_NO_PAGE) ? "free-list" : "");
   return QSA_OK;
 }
 
@@ -490,6 +493,120 @@ qsa_status_t qsa_sparse_attn_prefill(const void* q, qsa_dtype_t q_dt, const void
   return cuda_status(qsa::launch_sparse_attn(a, qsa::DecodePlan{}, nullptr, (cudaStream_t)stream,
                                              false),
                      "qsa_sparse_attn_prefill launch");
+}
+
+// ---- a dense chunk step: tables, rotary and cache write, attention ------------------
+
+size_t qsa_chunk_plan_workspace_size(int T, int B) {
+  (void)T; (void)B;
+  return 0;
+}
+
+qsa_status_t qsa_chunk_plan(const int32_t* n_cached, const int32_t* n_new, int B, const int32_t* free_pages, int n_free,
+                            int32_t* page_table, int pt_rows, int pt_stride, int num_pages, int T, int32_t* cu_new,
+                            int32_t* kv_len, int32_t* q_req, int32_t* q_pos, int32_t* slot, int32_t* n_taken,
+                            uint32_t* dev_status, qsa_stream_t stream) {
+  REQUIRE(B >= 0 && T >= 0 && n_free >= 0, "B, T and n_free must be >= 0 (got %d, %d, %d)", B, T, n_free);
+  SUPPORT(B <= qsa::chunk_plan_max_requests(), "B = %d exceeds %d requests per call", B, qsa::chunk_plan_max_requests());
+  SUPPORT(T <= kMaxChunkTokens, "T = %d exceeds %d tokens per call", T, kMaxChunkTokens);
+  REQUIRE(num_pages >= 1 && pt_rows >= 1 && pt_stride >= 1, "num_pages, pt_rows and pt_stride must be >= 1");
+  SUPPORT(num_pages <= kMaxPages, "num_pages = %d exceeds %d", num_pages, kMaxPages);
+  SUPPORT(pt_stride <= kMaxRowPages, "pt_stride = %d exceeds %d", pt_stride, kMaxRowPages);
+  REQUIRE(B <= pt_rows, "B = %d requests need as many page-table rows (got %d)", B, pt_rows);
+  if (B == 0 && T == 0) return QSA_OK;
+  REQUIRE(n_cached && n_new && page_table && cu_new && kv_len && n_taken, "null pointer argument");
+  REQUIRE(free_pages || n_free == 0, "free_pages is NULL with n_free = %d", n_free);
+  REQUIRE(T == 0 || (q_req && q_pos && slot), "null pointer argument");
+  qsa::PlanArgs a{n_cached, n_new, B, free_pages, n_free, page_table, pt_rows, pt_stride, num_pages, cu_new, kv_len,
+                  T, q_req, q_pos, slot, n_taken, dev_status};
+  return cuda_status(qsa::launch_chunk_plan(a, (cudaStream_t)stream), "qsa_chunk_plan launch");
+}
+
+size_t qsa_rope_write_workspace_size(int T, int Hq, int Hkv, int D) {
+  (void)T; (void)Hq; (void)Hkv; (void)D;
+  return 0;
+}
+
+qsa_status_t qsa_rope_write(const void* q, int q_stride, const void* k, int k_stride, const void* v, int v_stride,
+                            qsa_dtype_t x_dt, const int32_t* pos, int n_axes, int pos_stride, int sec0, int sec1,
+                            int sec2, int interleaved_axes, int adjacent_pairs, const float* inv_freq, int rot_dim,
+                            float rot_scale, const int32_t* slot, int T, int Hq, int Hkv, int D, void* q_out,
+                            void* k_pages, void* v_pages, qsa_dtype_t kv_dt, float k_scale, float v_scale,
+                            int num_pages, uint32_t* dev_status, qsa_stream_t stream) {
+  REQUIRE(T >= 0, "T must be >= 0 (got %d)", T);
+  SUPPORT(T <= kMaxChunkTokens, "T = %d exceeds %d tokens per call", T, kMaxChunkTokens);
+  REQUIRE(Hq >= 1 && Hkv >= 1, "Hq and Hkv must be >= 1 (got %d, %d)", Hq, Hkv);
+  SUPPORT(D == 64 || D == 128 || D == 256, "head dim D must be 64, 128 or 256 (got %d)", D);
+  SUPPORT((long long)Hq * D <= (1 << 24) && (long long)Hkv * D <= (1 << 24), "too many heads (Hq=%d, Hkv=%d)", Hq, Hkv);
+  REQUIRE(rot_dim >= 16 && rot_dim <= D && rot_dim % 16 == 0,
+          "rot_dim must be a multiple of 16 in 16 .. D (got %d, D = %d)", rot_dim, D);
+  REQUIRE(isfinite(rot_scale), "rot_scale must be finite");
+  REQUIRE(n_axes >= 1 && n_axes <= 3, "1 to 3 position axes (got %d)", n_axes);
+  REQUIRE(sec0 >= 0 && sec1 >= 0 && sec2 >= 0 && sec0 + (long long)sec1 + sec2 == rot_dim / 2,
+          "the axes' sections must be >= 0 and add up to rot_dim / 2 = %d (got %d, %d, %d)", rot_dim / 2, sec0, sec1,
+          sec2);
+  REQUIRE((n_axes >= 2 || sec1 == 0) && (n_axes >= 3 || sec2 == 0), "a section without an axis (%d axes: %d, %d, %d)",
+          n_axes, sec0, sec1, sec2);
+  REQUIRE(!interleaved_axes || (3 * sec1 - 2 < rot_dim / 2 && 3 * sec2 - 1 < rot_dim / 2),
+          "interleaved sections need 3 * sec1 - 2 and 3 * sec2 - 1 below rot_dim / 2 (got %d, %d)", sec1, sec2);
+  REQUIRE(n_axes == 1 || pos_stride >= T, "pos_stride %d is smaller than T %d", pos_stride, T);
+  REQUIRE(x_dt == QSA_F32 || x_dt == QSA_BF16, "q, k, v dtype must be F32 or BF16");
+  REQUIRE(kv_dt == QSA_F32 || kv_dt == QSA_BF16 || kv_dt == QSA_FP8_E4M3, "bad KV dtype");
+  if (kv_dt == QSA_FP8_E4M3)
+    REQUIRE(isfinite(k_scale) && isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f,
+            "FP8 scales must be finite and > 0");
+  REQUIRE(num_pages >= 1, "num_pages must be >= 1 (got %d)", num_pages);
+  SUPPORT(num_pages <= kMaxPages, "num_pages = %d exceeds %d", num_pages, kMaxPages);
+  REQUIRE(q_stride >= Hq * D && k_stride >= Hkv * D && v_stride >= Hkv * D,
+          "row strides (%d, %d, %d) are smaller than the rows", q_stride, k_stride, v_stride);
+  SUPPORT(q_stride % 8 == 0 && k_stride % 8 == 0 && v_stride % 8 == 0,
+          "row strides must be multiples of 8 values (got %d, %d, %d)", q_stride, k_stride, v_stride);
+  if (T == 0) return QSA_OK;
+  REQUIRE(q && k && v && pos && inv_freq && slot && q_out && k_pages && v_pages, "null pointer argument");
+  REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(q_out) && aligned16(k_pages) && aligned16(v_pages),
+          "q, k, v, q_out, k_pages and v_pages must be 16-byte aligned");
+  qsa::RopeArgs a{q, k, v, x_dt, q_stride, k_stride, v_stride, pos, n_axes, pos_stride, sec0, sec1, sec2,
+                  interleaved_axes, adjacent_pairs, inv_freq, rot_dim, rot_scale, slot, T, Hq, Hkv, D, q_out, k_pages,
+                  v_pages, kv_dt, k_scale, v_scale, num_pages, dev_status};
+  return cuda_status(qsa::launch_rope_write(a, (cudaStream_t)stream), "qsa_rope_write launch");
+}
+
+size_t qsa_chunk_attn_workspace_size(int T, int B, int Hq, int Hkv, int D, qsa_dtype_t kv_dt) {
+  return qsa::chunk_attn_ws_bytes(T, B, Hq, Hkv, D, kv_dt);
+}
+
+qsa_status_t qsa_chunk_attn(const void* q, qsa_dtype_t q_dt, const void* k_pages, const void* v_pages,
+                            qsa_dtype_t kv_dt, float k_scale, float v_scale, int num_pages, const int32_t* page_table,
+                            int pt_rows, int pt_stride, const int32_t* cu_new, const int32_t* kv_len, int B, int T,
+                            int Hq, int Hkv, int D, float sm_scale, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, uint32_t* dev_status, qsa_stream_t stream) {
+  REQUIRE(T >= 0 && B >= 0, "T and B must be >= 0 (got %d, %d)", T, B);
+  SUPPORT(T <= kMaxChunkTokens, "T = %d exceeds %d tokens per call", T, kMaxChunkTokens);
+  SUPPORT(B <= qsa::chunk_attn_max_requests(), "B = %d exceeds %d requests per call", B, qsa::chunk_attn_max_requests());
+  REQUIRE(Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0, "need Hq %% Hkv == 0 (Hq=%d, Hkv=%d)", Hq, Hkv);
+  SUPPORT(Hq / Hkv <= 16, "at most 16 query heads per KV head (got %d)", Hq / Hkv);
+  SUPPORT(D == 64 || D == 128 || D == 256, "head dim D must be 64, 128 or 256 (got %d)", D);
+  SUPPORT((long long)Hq * D <= (1 << 24), "too many heads (Hq=%d)", Hq);
+  REQUIRE(num_pages >= 1 && pt_rows >= 1 && pt_stride >= 1, "num_pages, pt_rows and pt_stride must be >= 1");
+  SUPPORT(num_pages <= kMaxPages, "num_pages = %d exceeds %d", num_pages, kMaxPages);
+  SUPPORT(pt_stride <= kMaxRowPages, "pt_stride = %d exceeds %d", pt_stride, kMaxRowPages);
+  REQUIRE(B <= pt_rows, "B = %d requests need as many page-table rows (got %d)", B, pt_rows);
+  REQUIRE(q_dt == QSA_F32 || q_dt == QSA_BF16, "q dtype must be F32 or BF16");
+  REQUIRE(kv_dt == QSA_F32 || kv_dt == QSA_BF16 || kv_dt == QSA_FP8_E4M3, "bad KV dtype");
+  if (kv_dt == QSA_FP8_E4M3)
+    REQUIRE(isfinite(k_scale) && isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f,
+            "FP8 scales must be finite and > 0");
+  REQUIRE(isfinite(sm_scale), "sm_scale must be finite");
+  if (T == 0 || B == 0) return QSA_OK;
+  REQUIRE(q && k_pages && v_pages && page_table && cu_new && kv_len && out, "null pointer argument");
+  REQUIRE(aligned16(q) && aligned16(k_pages) && aligned16(v_pages) && aligned16(out),
+          "q, k_pages, v_pages and out must be 16-byte aligned");
+  const size_t need = qsa_chunk_attn_workspace_size(T, B, Hq, Hkv, D, kv_dt);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
+    return fail(QSA_ERR_WORKSPACE, "qsa_chunk_attn needs a 16-byte aligned workspace of %zu bytes", need);
+  qsa::ChunkArgs a{q, q_dt, k_pages, v_pages, kv_dt, k_scale, v_scale, num_pages, page_table, pt_rows, pt_stride,
+                   cu_new, kv_len, B, T, Hq, Hkv, D, sm_scale, out, lse, dev_status};
+  return cuda_status(qsa::launch_chunk_attn(a, workspace, (cudaStream_t)stream), "qsa_chunk_attn launch");
 }
 
 }  // extern "C"

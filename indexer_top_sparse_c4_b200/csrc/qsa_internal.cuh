@@ -322,6 +322,36 @@ cudaError_t launch_dcp_expand(const int32_t* sel, const int32_t* n_sel, int K, c
 cudaError_t launch_dcp_merge_attn(const float* o_parts, const float* lse_parts, int R, int T, int Hq, int D,
                                   void* out, qsa_dtype_t out_dt, float* lse, cudaStream_t s);
 
+// Block tables and slot maps of a step (chunk_plan.cu).
+struct PlanArgs {
+  const int32_t* n_cached; const int32_t* n_new; int B; const int32_t* free_pages; int n_free;
+  int32_t* page_table; int pt_rows, pt_stride, num_pages; int32_t* cu_new; int32_t* kv_len; int T;
+  int32_t* q_req; int32_t* q_pos; int32_t* slot; int32_t* n_taken; uint32_t* status;
+};
+int chunk_plan_max_requests();
+cudaError_t launch_chunk_plan(const PlanArgs& a, cudaStream_t s);
+
+// Rotary positions and the cache write (rope_write.cu).
+struct RopeArgs {
+  const void* q; const void* k; const void* v; qsa_dtype_t x_dt; int q_stride, k_stride, v_stride;
+  const int32_t* pos; int n_axes, pos_stride; int sec0, sec1, sec2; int interleaved_axes, adjacent_pairs;
+  const float* inv_freq; int rot_dim; float rot_scale; const int32_t* slot; int T, Hq, Hkv, D;
+  void* q_out; void* k_pages; void* v_pages; qsa_dtype_t kv_dt; float k_scale, v_scale; int num_pages;
+  uint32_t* status;
+};
+cudaError_t launch_rope_write(const RopeArgs& a, cudaStream_t s);
+
+// Causal attention of the requests' new tokens over a paged cache (chunk_attn.cu).
+struct ChunkArgs {
+  const void* q; qsa_dtype_t q_dt; const void* k_pages; const void* v_pages; qsa_dtype_t kv_dt;
+  float k_scale, v_scale; int num_pages; const int32_t* page_table; int pt_rows, pt_stride;
+  const int32_t* cu_new; const int32_t* kv_len; int B, T, Hq, Hkv, D; float sm_scale;
+  void* out; float* lse; uint32_t* status;
+};
+int chunk_attn_max_requests();
+size_t chunk_attn_ws_bytes(int T, int B, int Hq, int Hkv, int D, qsa_dtype_t kv_dt);
+cudaError_t launch_chunk_attn(const ChunkArgs& a, void* ws, cudaStream_t s);
+
 // Sets the message qsa_last_error_string() returns on this thread.
 void set_last_error(const char* msg);
 // The host-side argument checks of the attention calls (shapes, dtypes,

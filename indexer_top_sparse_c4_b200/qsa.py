@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(_PKG, "libqsa.so")
  QSA_ERR_DEVICE_INDEX, QSA_ERR_TIMEOUT) = range(7)
 QSA_F32, QSA_BF16, QSA_FP8_E4M3 = 0, 1, 2
 QSA_DEV_BAD_PAGE, QSA_DEV_BAD_TOKEN, QSA_DEV_BAD_GROUP, QSA_DEV_ROW_RANGE = 1, 2, 4, 8
-QSA_DEV_BAD_REQUEST, QSA_DEV_TIMEOUT = 16, 32
+QSA_DEV_BAD_REQUEST, QSA_DEV_TIMEOUT, QSA_DEV_NO_PAGE = 16, 32, 64
 QSA_PREFIX_HIST_BINS = 4096
 
 ENTRY_POINTS = (
@@ -35,6 +35,8 @@ ENTRY_POINTS = (
     "qsa_sparse_attn_prefill_workspace_size", "qsa_sparse_attn_prefill", "qsa_get_device_status",
     "qsa_dcp_shard_positions", "qsa_dcp_candidates", "qsa_dcp_merge_topk", "qsa_dcp_expand",
     "qsa_dcp_merge_attn", "qsa_selftest_bounded_wait",
+    "qsa_chunk_plan_workspace_size", "qsa_chunk_plan", "qsa_rope_write_workspace_size", "qsa_rope_write",
+    "qsa_chunk_attn_workspace_size", "qsa_chunk_attn",
     "qsa_last_error_string", "qsa_status_name", "qsa_abi_version",
 )
 
@@ -158,6 +160,16 @@ def lib() -> ctypes.CDLL:
     for name in ("qsa_index_scores", "qsa_topk_groups", "qsa_expand_select", "qsa_topk_expand",
                  "qsa_sparse_attn_decode", "qsa_sparse_attn_prefill"):
         getattr(L, name).restype = I
+    L.qsa_chunk_plan_workspace_size.argtypes = [I, I]
+    L.qsa_chunk_plan.argtypes = [P, P, I, P, I, P, I, I, I, I, P, P, P, P, P, P, P, P]
+    L.qsa_rope_write_workspace_size.argtypes = [I, I, I, I]
+    L.qsa_rope_write.argtypes = [P, I, P, I, P, I, I, P, I, I, I, I, I, I, I, P, I, F, P, I, I, I, I, P, P, P, I, F, F,
+                                 I, P, P]
+    L.qsa_chunk_attn_workspace_size.argtypes = [I, I, I, I, I, I]
+    L.qsa_chunk_attn.argtypes = [P, I, P, P, I, F, F, I, P, I, I, P, P, I, I, I, I, I, F, P, P, P, U, P, P]
+    for name in ("qsa_chunk_plan", "qsa_rope_write", "qsa_chunk_attn"):
+        getattr(L, name).restype = I
+        getattr(L, name + "_workspace_size").restype = U
     L.qsa_last_error_string.restype = ctypes.c_char_p
     L.qsa_status_name.restype = ctypes.c_char_p
     L.qsa_status_name.argtypes = [I]
@@ -457,4 +469,139 @@ def qsa_dcp_merge_attn(o_parts, lse_parts, out, lse=None, stream=None):
     R, T, Hq, D = o_parts.shape
     _check(lib().qsa_dcp_merge_attn(_ptr(o_parts), _ptr(lse_parts), R, T, Hq, D, _ptr(out), _dt(out), _ptr(lse),
                                     _stream(stream)))
+    return out
+
+
+# ---- a dense chunk step: tables, rotary and cache write, attention --------------------
+
+def _same_device(anchor, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != anchor.device:
+            raise ValueError(f"{name} is on {t.device}, the call runs on {anchor.device}")
+
+
+def _int32(**tensors):
+    for name, t in tensors.items():
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32 (got {t.dtype})")
+
+
+def _call(fn, anchor, stream, *args):
+    """One library call on the device of its tensors, whichever is current;
+    stream None: that device's current stream."""
+    if anchor.is_cuda and anchor.device.index != torch.cuda.current_device():
+        with torch.cuda.device(anchor.device):
+            _check(fn(*args, _stream(stream)))
+    else:
+        _check(fn(*args, _stream(stream)))
+
+
+def qsa_chunk_plan(n_cached, n_new, free_pages, page_table, num_pages, cu_new, kv_len, q_req, q_pos, slot, n_taken,
+                   dev_status=None, stream=None):
+    """Block tables and slot maps of a step from its requests' lengths (all
+    tensors int32; T = the size of q_req, q_pos and slot).  Fills cu_new
+    [B + 1], kv_len [B], q_req / q_pos / slot [T] (-1 behind the last token),
+    n_taken [1] and the new entries of page_table."""
+    B, T = n_cached.numel(), slot.numel()
+    _int32(n_cached=n_cached, n_new=n_new, free_pages=free_pages, page_table=page_table, cu_new=cu_new, kv_len=kv_len,
+           q_req=q_req, q_pos=q_pos, slot=slot, n_taken=n_taken)
+    _same_device(page_table, n_cached=n_cached, n_new=n_new, free_pages=free_pages, cu_new=cu_new, kv_len=kv_len,
+                 q_req=q_req, q_pos=q_pos, slot=slot, n_taken=n_taken, dev_status=dev_status)
+    if (n_new.numel() != B or kv_len.numel() != B or cu_new.numel() != B + 1 or q_req.numel() != T
+            or q_pos.numel() != T or n_taken.numel() < 1 or page_table.dim() != 2):
+        raise ValueError("shapes: n_cached, n_new, kv_len [B], cu_new [B + 1], q_req, q_pos, slot [T], n_taken [1], "
+                         "page_table [pt_rows, pt_stride]")
+    _call(lib().qsa_chunk_plan, page_table, stream, _ptr(n_cached), _ptr(n_new), B, _ptr(free_pages),
+          free_pages.numel(), _ptr(page_table), page_table.shape[0], page_table.shape[1], int(num_pages), T, _ptr(cu_new),
+          _ptr(kv_len), _ptr(q_req), _ptr(q_pos), _ptr(slot), _ptr(n_taken), _ptr(dev_status))
+    return cu_new, kv_len, q_req, q_pos, slot, n_taken
+
+
+def _rows(name, x, T, H, D):
+    """(pointer, row stride) of x [T, H, D] whose rows may be strided."""
+    if tuple(x.shape) != (T, H, D):
+        raise ValueError(f"{name} must be [{T}, {H}, {D}] (got {list(x.shape)})")
+    if x.stride(2) != 1 or (H > 1 and x.stride(1) != D):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return ctypes.c_void_p(x.data_ptr()), (x.stride(0) if T > 1 else H * D)
+
+
+def _cache_shape(k_pages, v_pages, Hkv, D):
+    if (k_pages.dim() != 4 or tuple(k_pages.shape[1:]) != (64, Hkv, D) or k_pages.shape != v_pages.shape
+            or k_pages.dtype != v_pages.dtype):
+        raise ValueError(f"k_pages and v_pages must be [num_pages, 64, {Hkv}, {D}] of one dtype")
+
+
+def qsa_rope_write(q, k, v, pos, inv_freq, slot, q_out, k_pages, v_pages, sections=None, interleaved_axes=False,
+                   adjacent_pairs=False, rot_scale=1.0, k_scale=1.0, v_scale=1.0, dev_status=None, stream=None):
+    """Rotary positions on q [T, Hq, D] and k [T, Hkv, D] (rows may be slices of
+    one projection's output) and the write of k and v to rows slot [T] of the
+    caches.  pos: int32 [T], or [n_axes, T] with up to three axes; sections:
+    frequencies per axis, adding up to rot_dim / 2 = inv_freq.numel()."""
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    half = inv_freq.numel()
+    axes = 1 if pos.dim() == 1 else pos.shape[0]
+    sec = [int(n) for n in (sections if sections is not None else (half,))]
+    if axes > 1 and sections is None:
+        raise ValueError("several axes need their sections")
+    sec += [0] * (3 - len(sec))
+    if len(sec) != 3 or not 1 <= axes <= 3:
+        raise ValueError("one to three axes and sections")
+    _int32(pos=pos, slot=slot)
+    if pos.shape[-1] != T or slot.numel() != T or pos.dim() > 2:
+        raise ValueError(f"pos must be [{T}] or [n_axes, {T}], slot [{T}]")
+    if T > 1 and pos.stride(-1) != 1:
+        raise ValueError("the positions of an axis must be contiguous")
+    if inv_freq.dtype != torch.float32:
+        raise TypeError("inv_freq must be float32")
+    if not (q.dtype == k.dtype == v.dtype == q_out.dtype):
+        raise TypeError("q, k, v and q_out must have one dtype")
+    if tuple(q_out.shape) != (T, Hq, D):
+        raise ValueError("q_out must have q's shape")
+    _cache_shape(k_pages, v_pages, Hkv, D)
+    _same_device(k_pages, q=q, k=k, v=v, pos=pos, inv_freq=inv_freq, slot=slot, q_out=q_out, v_pages=v_pages,
+                 dev_status=dev_status)
+    qp, qs = _rows("q", q, T, Hq, D)
+    kp, ks = _rows("k", k, T, Hkv, D)
+    vp, vs = _rows("v", v, T, Hkv, D)
+    _call(lib().qsa_rope_write, k_pages, stream, qp, qs, kp, ks, vp, vs, _dt(q), ctypes.c_void_p(pos.data_ptr()), axes,
+          pos.stride(0) if axes > 1 else T, *sec, int(bool(interleaved_axes)), int(bool(adjacent_pairs)),
+          _ptr(inv_freq), 2 * half, float(rot_scale), _ptr(slot), T, Hq, Hkv, D, _ptr(q_out), _ptr(k_pages),
+          _ptr(v_pages), _dt(k_pages), float(k_scale), float(v_scale), k_pages.shape[0], _ptr(dev_status))
+    return q_out
+
+
+def qsa_chunk_attn_workspace_size(T, B, Hq, Hkv, D, kv_dtype=QSA_BF16) -> int:
+    """Bytes of workspace qsa_chunk_attn needs; kv_dtype is a QSA_* code or a
+    torch dtype of the KV cache."""
+    if isinstance(kv_dtype, torch.dtype):
+        kv_dtype = _dt(torch.empty(0, dtype=kv_dtype))
+    return int(lib().qsa_chunk_attn_workspace_size(T, B, Hq, Hkv, D, kv_dtype))
+
+
+def qsa_chunk_attn(q, k_pages, v_pages, page_table, cu_new, kv_len, out, workspace=None, k_scale=1.0, v_scale=1.0,
+                   sm_scale=0.0, lse=None, dev_status=None, stream=None):
+    """Causal attention of every request's new tokens (rows cu_new[b] ..
+    cu_new[b+1] - 1 of q [T, Hq, D]) over its kv_len[b] cached tokens."""
+    T, Hq, D = q.shape
+    B = kv_len.numel()
+    _int32(page_table=page_table, cu_new=cu_new, kv_len=kv_len)
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages and v_pages must be [num_pages, 64, Hkv, D]")
+    Hkv = k_pages.shape[2]
+    _cache_shape(k_pages, v_pages, Hkv, D)
+    if cu_new.numel() != B + 1 or page_table.dim() != 2:
+        raise ValueError("shapes: kv_len [B], cu_new [B + 1], page_table [pt_rows, pt_stride]")
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    if lse is not None and (tuple(lse.shape) != (T, Hq) or lse.dtype != torch.float32):
+        raise ValueError("lse must be float32 [T, Hq]")
+    _same_device(q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, cu_new=cu_new, kv_len=kv_len, out=out,
+                 workspace=workspace, lse=lse, dev_status=dev_status)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(lib().qsa_chunk_attn, q, stream, _ptr(q), _dt(q), _ptr(k_pages), _ptr(v_pages), _dt(k_pages), float(k_scale),
+          float(v_scale), k_pages.shape[0], _ptr(page_table), page_table.shape[0], page_table.shape[1], _ptr(cu_new),
+          _ptr(kv_len), B, T, Hq, Hkv, D, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+          _ptr(dev_status))
     return out
