@@ -1,6 +1,681 @@
+// chunk_attn_tc.cu -- the chunk attention on the 5th-generation tensor cores:
+// BF16 queries over a BF16 or FP8 E4M3 paged cache, single tokens to whole
+// prompts.
+//
+//   S = Q K^T (FP32),  P = exp2(scale log2(e) S - m),  O += P V,  l += sum P
+//
+// with m a running reference of the row's maximum.  All P, l and O of a row
+// share one reference, so the result O / l does not depend on it; it is moved
+// (and O, l rescaled) only when the maximum has grown by more than 2^8 over
+// it, which keeps P in range of its 16-bit type and leaves O in TMEM alone in
+// almost every step.
+//
+// sm_100a design, one persistent CTA per SM:
+//  * tile: M = 128 query rows (one TMEM lane each) x N = 128 keys (two pages).
+//    The rows are whole tokens: all G = Hq / Hkv query heads of a KV head, so
+//    a key or value read once serves 128 / G tokens x G heads; a decode step
+//    uses G of the rows and is bound by the cache read.
+//  * TMEM (512 columns): O in columns 0 .. D-1, two S tiles of 128 columns; P
+//    overwrites its S tile (16-bit, half the columns) and is the A operand of
+//    P V straight from TMEM.
+//  * keys and values stream through one ring of 16 KB slots (128 tokens x 64
+//    columns, 128-byte swizzle): a K tile is D / 64 slots, the K-major B
+//    operand of S; a V tile is D / 64 slots, each the MN-major B operand of 64
+//    columns of O.  Order K0, K1, V0, K2, V1, ...: S of the next tile is
+//    computed while the softmax of this one runs.
+//  * warp 0 issues the TMA loads (one box per page and slot, pages looked up
+//    32 at a time), warp 1 the MMAs, warps 4..11 the softmax (two warps per
+//    TMEM lane quarter, 64 keys each: the two exchange row maxima through
+//    shared memory).
+//  * FP8 cache: boxes of codes land in a second ring, and warps 12..15 turn
+//    them into FP16 slots (e4m3 is a subset of FP16, the product P V then
+//    takes P in FP16).  The query is FP16 too: each row is scaled by a power
+//    of two that puts its largest value at 2^10 .. 2^11, which keeps all bits
+//    of every BF16 value down to 2^-24 of the row's largest; the scale is
+//    undone in FP32 with the softmax scale.
+//  * tiles that hold keys some row must not see ("edge" tiles: the causal
+//    diagonal, the last page): masked P is 0, but 0 x NaN is NaN in the matrix
+//    product, so the softmax warps first clear the value rows past the last
+//    token and any non-finite value of the tile from its V slots.  Non-finite
+//    values that a row does see are added back to its output at the end (the
+//    `poison` flag; the sum is then non-finite whatever its weight).
+//  * few tiles: the (tile, key block) space is divided evenly over the CTAs and
+//    a combine kernel merges shared tiles; many tiles: one CTA per tile.
+//  * every wait is bounded (mbarrier.cuh); after a time-out the warps finish
+//    their loops without waiting, in-flight copies and MMAs are drained, and
+//    TMEM is released.
+#include <cuda.h>
+
 #include "chunk_common.cuh"
+#include "umma.cuh"
+
 namespace qsa {
-bool chunk_tc_supported(const ChunkArgs&) { return false; }
-int chunk_tc_rows() { return 128; }
-cudaError_t launch_chunk_attn_tc(const ChunkArgs&, const ChunkWs&, int, float, float, cudaStream_t) { return cudaErrorNotSupported; }
+namespace {
+
+using namespace mbar;
+
+constexpr int kRows = 128;
+constexpr int kKeys = 128;               // keys of a tile: two pages
+constexpr int kSlotBytes = kKeys * 128;  // 128 tokens x 64 16-bit columns
+constexpr int kRawBytes = kKeys * 64;    // 128 tokens x 64 codes
+constexpr uint32_t kSCol = 256;          // first TMEM column of the S tiles
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSoftWarps = 8;
+constexpr float kGrow = 8.f;             // log2 of how far P may grow before O is rescaled
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <int D, bool FP8>
+struct Cfg {
+  static constexpr int DB = D / 64;   // slots of a tile (the edge tiles' waits need 1.5 tiles of ring)
+  // Q + rings take 208 KB: nine BF16 slots at D = 256 (2.25 tiles ahead)
+  static constexpr int kSlots = FP8 ? (D == 256 ? 6 : 8) : (D == 256 ? 9 : D == 128 ? 11 : 12);
+  static constexpr int kRaw = FP8 ? 6 : 0;
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  static constexpr int kQBytes = DB * kRows * 128;
+};
+
+template <int D, bool FP8>
+struct TcSmem {
+  using C = Cfg<D, FP8>;
+  alignas(1024) unsigned char q[C::kQBytes];
+  alignas(1024) unsigned char slot[C::kSlots][kSlotBytes];
+  alignas(1024) unsigned char raw[C::kRaw ? C::kRaw : 1][C::kRaw ? kRawBytes : 16];
+  alignas(8) uint64_t full[C::kSlots], empty[C::kSlots];
+  // s_full, p_full and pv_done count tiles, one of each two: a waiter is never
+  // more than one phase ahead of a barrier, so a phase's parity names it
+  uint64_t raw_full[C::kRaw ? C::kRaw : 1], raw_empty[C::kRaw ? C::kRaw : 1];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, drain;
+  float mx[2][2][kRows];                 // [tile parity][half][row] maxima
+  float lx[2][kRows];                    // [half][row] sums
+  float q_scale[kRows];                  // FP8: what undoes the row's power of two
+  int poison[3];                         // by item, modulo 3
+  uint32_t tmem_base;
+  int abort_flag;
+  ChunkSched sched;
+};
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(saddr(dst)), "l"(map), "r"(saddr(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// A and B in shared memory / A in TMEM
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  umma::mma_bf16(d, a, b, idesc, acc);   // kind::f16: the operand type is idesc's
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// kind::f16 instruction descriptor: F32 accumulators, M = 128; f16 or bf16
+// operands; B K-major (keys of S) or MN-major (values)
+constexpr uint32_t idesc(bool f16, int N, bool b_mn) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(kRows >> 4) << 24);
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
+      "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]),
+      "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]),
+      "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool FP8>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if constexpr (FP8) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A wait that gives up at once when the CTA is stopping.
+__device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+  if (*abort_flag) return false;
+  return mbar_wait(b, parity, abort_flag, status);
+}
+// The same by a whole warp, which is converged on return (the TMEM loads and
+// stores that follow need it).
+__device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+  return __all_sync(0xffffffffu, wait(b, parity, abort_flag, status));
+}
+
+// The physical token row of logical page lp of a request, or the first row
+// past the cache (TMA then fills zeros) when no token needs it or it is bad.
+__device__ __forceinline__ int page_row(const ChunkArgs& a, const int32_t* pt, int lp, int n_pages, bool report) {
+  if (lp >= n_pages) return a.num_pages * kPageTokens;
+  const int page = __ldg(pt + lp);
+  if (page < 0 || page >= a.num_pages) {
+    if (report) flag(a.status, QSA_DEV_BAD_PAGE);
+    return a.num_pages * kPageTokens;
+  }
+  return page * kPageTokens;
+}
+
+template <bool FP8>
+__device__ __forceinline__ uint32_t nonfinite16(uint32_t w) {  // mask of the non-finite halves of w
+  constexpr uint32_t e = FP8 ? 0x7c00u : 0x7f80u;
+  return ((w & e) == e ? 0xffffu : 0u) | ((w & (e << 16)) == (e << 16) ? 0xffff0000u : 0u);
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
+    chunk_tc_kernel(ChunkArgs a, ChunkWs ws, float qk_scale_log2, float vmul, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v) {
+  using C = Cfg<D, FP8>;
+  constexpr int DB = C::DB;
+  static_assert(2 * C::kSlots >= 3 * DB, "see the edge tiles");
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  TcSmem<D, FP8>& sm = *reinterpret_cast<TcSmem<D, FP8>*>(smem_raw + ((1024 - ((uintptr_t)smem_raw & 1023)) & 1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm.abort_flag;
+  const int G = a.Hq / a.Hkv, TPT = kRows / G;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&sm.full[s], FP8 ? 4 : 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int s = 0; s < C::kRaw; ++s) {
+      mbar_init(&sm.raw_full[s], 1);
+      mbar_init(&sm.raw_empty[s], 4);
+    }
+    mbar_init(&sm.q_full, kSoftWarps);
+    mbar_init(&sm.q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.p_full[s], kSoftWarps);
+      mbar_init(&sm.pv_done[s], 1);
+    }
+    mbar_init(&sm.o_free, kSoftWarps);
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    sm.poison[0] = sm.poison[1] = sm.poison[2] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sm.tmem_base)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) ws.desc[blockIdx.x].n_parts = 0;
+  chunk_sched_build(a, sm.sched, TPT, kKeys);
+  ChunkWalk walk;
+  walk.begin(a, sm.sched);
+  ChunkItem it;
+  uint32_t s = 0, phase = 0;   // ring position of the loading, issuing and converting warps
+  bool ok = true, issued = false;
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    constexpr int kRing = FP8 ? C::kRaw : C::kSlots;
+    constexpr uint32_t kBytes = FP8 ? kRawBytes : kSlotBytes;
+    uint64_t* const fulls = FP8 ? sm.raw_full : sm.full;
+    uint64_t* const empties = FP8 ? sm.raw_empty : sm.empty;
+    while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
+      const int n = it.blk_hi - it.blk_lo, lp0 = 2 * it.blk_lo;
+      const int n_pages = (it.kv + kPageTokens - 1) / kPageTokens;
+      const int32_t* pt = a.page_table + (size_t)it.b * a.pt_stride;
+      // rows of pages 32 w .. 32 w + 31 of this piece, and the next 32
+      int win = 0, last_lp = lp0 + 2 * n;
+      int cur = page_row(a, pt, lp0 + lane, min(n_pages, last_lp), true);
+      int nxt = page_row(a, pt, lp0 + 32 + lane, min(n_pages, last_lp), true);
+      auto load_tile = [&](const CUtensorMap* map, int j) {
+        const int x = 2 * j, from = (x >> 5) == win ? cur : nxt;
+        const int y0 = __shfl_sync(0xffffffffu, from, x & 31), y1 = __shfl_sync(0xffffffffu, from, (x + 1) & 31);
+        for (int db = 0; db < DB; ++db) {
+          ok = wait_warp(&empties[s], phase ^ 1, abort_flag, a.status);
+          if (!ok) return;
+          if (lane == 0) {
+            unsigned char* dst = FP8 ? sm.raw[s] : sm.slot[s];
+            mbar_arrive_tx(&fulls[s], kBytes);
+            tma_load_3d(dst, map, &fulls[s], db * 64, it.kvh, y0);
+            tma_load_3d(dst + kBytes / 2, map, &fulls[s], db * 64, it.kvh, y1);
+          }
+          if (++s == kRing) s = 0, phase ^= 1;
+        }
+      };
+      load_tile(&map_k, 0);
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n) load_tile(&map_k, j + 1);
+        if (ok) load_tile(&map_v, j);
+        if (((2 * j + 2) >> 5) != win) {   // the next V tile lies in the next window
+          ++win;
+          cur = nxt;
+          nxt = page_row(a, pt, lp0 + 32 * (win + 1) + lane, min(n_pages, last_lp), true);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    constexpr uint32_t kIdS = idesc(FP8, kKeys, false), kIdO = idesc(FP8, 64, true);
+    const uint64_t qd = umma::smem_desc(saddr(sm.q));
+    uint32_t g = 0, item = 0;
+    auto step = [&]() { if (++s == C::kSlots) s = 0, phase ^= 1; };
+    auto qk = [&](uint32_t buf) {
+      for (int db = 0; db < DB; ++db) {
+        ok = ok && wait_warp(&sm.full[s], phase, abort_flag, a.status);
+        if (!ok) return;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint64_t kd = umma::smem_desc(saddr(sm.slot[s]));
+          const uint64_t qa = qd + (uint64_t)(db * (kRows * 128) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ss(tmem + kSCol + buf * kKeys, qa + ks * 2, kd + ks * 2, kIdS, (db | ks) != 0);
+          umma::commit(&sm.empty[s]);
+          if (db == DB - 1) umma::commit(&sm.s_full[buf]);
+          issued = true;
+        }
+        __syncwarp();
+        step();
+      }
+    };
+    auto pv = [&](uint32_t buf, bool first) {
+      for (int db = 0; db < DB; ++db) {
+        ok = ok && wait_warp(&sm.full[s], phase, abort_flag, a.status);
+        if (!ok) return;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint64_t vd = umma::smem_desc(saddr(sm.slot[s]));
+          const uint32_t p = tmem + kSCol + buf * kKeys;
+          // 16 keys a step: 8 columns of P, 16 rows (2 KB) of V; keys 64.. of P start 64 columns on
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts(tmem + db * 64, p + (ks >> 2) * 64 + (ks & 3) * 8, vd + ks * 128, kIdO, !first || ks != 0);
+          umma::commit(&sm.empty[s]);
+          if (db == DB - 1) umma::commit(&sm.pv_done[buf]);
+          issued = true;
+        }
+        __syncwarp();
+        step();
+      }
+    };
+    while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
+      const int n = it.blk_hi - it.blk_lo;
+      ok = wait_warp(&sm.q_full, item & 1, abort_flag, a.status);
+      if (ok) qk(g & 1);
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n) qk((g + j + 1) & 1);
+        if (!ok) break;
+        if (j + 2 >= n && (j + 1 < n || n == 1) && lane == 0) umma::commit(&sm.q_empty);  // after the last Q K^T
+        __syncwarp();
+        // the previous item's O has been read out before the first P V
+        if (j == 0) ok = wait_warp(&sm.o_free, (item & 1) ^ 1, abort_flag, a.status);
+        ok = ok && wait_warp(&sm.p_full[(g + j) & 1], ((g + j) >> 1) & 1, abort_flag, a.status);
+        if (ok) pv((g + j) & 1, j == 0);
+      }
+      g += n;
+      ++item;
+    }
+  } else if (warp >= 4 && warp < 4 + kSoftWarps) {
+    // ---------------- softmax, correction, epilogue ----------------
+    const int st = threadIdx.x - 128;                  // 0 .. 255
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const int row = 32 * quarter + lane;
+    const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
+    constexpr int OC = D / 2;                          // columns of O per thread
+    uint32_t g = 0, item = 0, item3 = 0, seq = 0;                 // tiles, items, slots (of two rounds) so far
+
+    // Q of the next item into shared memory (128-byte swizzle, K-major); rows
+    // past its tokens are zero
+    auto load_q = [&](const ChunkItem& x) -> float {
+      wait_warp(&sm.q_empty, (item & 1) ^ 1, abort_flag, a.status);
+      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
+      constexpr int CH = D / 8;                        // 16-byte chunks per row
+      const int rows = x.ntok * G;
+#pragma unroll 4
+      for (int i = st; i < kRows * CH; i += 256) {
+        const int r = i / CH, c = i % CH;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < rows)
+          v = *reinterpret_cast<const uint4*>(q + ((size_t)(x.t0 + r / G) * a.Hq + x.kvh * G + r % G) * D + c * 8);
+        if constexpr (FP8) {
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t top = 0;                            // the row's largest exponent field
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = max(top, max((w[k] >> 7) & 0xffu, (w[k] >> 23) & 0xffu));
+#pragma unroll
+          for (int d = 1; d < CH; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const uint32_t E = min(max(top, 11u), 254u);
+          const float up = __uint_as_float((264u - E) << 23);    // 2^(137 - E): the largest lands in 2^10 .. 2^11
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = pack16<true>(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+          if (c == 0) sm.q_scale[r] = __uint_as_float((E - 10u) << 23);  // 2^(E - 137)
+        }
+        *reinterpret_cast<uint4*>(sm.q + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+      }
+      async_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+      float sc = qk_scale_log2;
+      if constexpr (FP8) {
+        bar_sync(5, 256);
+        sc = fmaxf(sc * sm.q_scale[row], 1.2e-38f);   // 0 x -inf below would be NaN; the logits are 0 either way
+      }
+      return sc;
+    };
+
+    ChunkItem nx;
+    bool have = walk.next(a, sm.sched, TPT, kKeys, it);
+    float sc_next = have ? load_q(it) : 0.f;
+    while (have) {
+      const float sc = sc_next;
+      const int n = it.blk_hi - it.blk_lo, rows = it.ntok * G;
+      const int tok = row / G;
+      const bool live = row < rows;                    // this thread's row is a query
+      const bool warp_live = 32 * quarter < rows;
+      const int lim = live ? min(it.p0 + tok + 1, it.kv) : 0;   // keys the row sees
+      const int lim0 = min(it.p0 + 1, it.kv);          // keys the tile's first row sees (the fewest)
+      const int n_pages = (it.kv + kPageTokens - 1) / kPageTokens;
+      const int32_t* pt = a.page_table + (size_t)it.b * a.pt_stride;
+      float m = -INFINITY, l = 0.f;
+      int prow = page_row(a, pt, 2 * it.blk_lo + half, n_pages, false);   // this half's page of the tile
+      for (int j = 0; j < n; ++j) {
+        const uint32_t buf = (g + j) & 1;
+        const int key0 = (it.blk_lo + j) * kKeys + half * 64;
+        const int prow_next = j + 1 < n ? page_row(a, pt, 2 * (it.blk_lo + j + 1) + half, n_pages, false) : 0;
+        wait_warp(&sm.s_full[buf], ((g + j) >> 1) & 1, abort_flag, a.status);
+        tc_fence_after();
+        if (warp_live) {
+          float s[64];
+          const uint32_t ta = tlane + kSCol + buf * kKeys + half * 64;
+          tmem_ld32(ta, s);
+          tmem_ld32(ta + 32, s + 32);
+          tmem_wait_ld();
+          const int seen = prow < a.num_pages * kPageTokens ? lim - key0 : 0;
+          if (__any_sync(0xffffffffu, seen < 64)) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) s[i] = i < seen ? s[i] : -INFINITY;
+          }
+          float mx = s[0];
+#pragma unroll
+          for (int i = 1; i < 64; ++i) mx = fmaxf(mx, s[i]);
+          sm.mx[buf][half][row] = mx;
+          bar_sync(1 + quarter, 64);
+          mx = fmaxf(mx, sm.mx[buf][half ^ 1][row]) * sc;
+          // move the reference where the maximum has outgrown it
+          const bool grow = mx > m + kGrow || (m == -INFINITY && mx > m);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = fmaxf(m, mx);
+            const float alpha = m == mn ? 1.f : ex2(m - mn);
+            m = mn;
+            l *= alpha;
+            if (j > 0) {
+              wait_warp(&sm.pv_done[buf ^ 1], ((g + j - 1) >> 1) & 1, abort_flag, a.status);
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < OC; c += 32) {
+                float o[32];
+                tmem_ld32(tlane + half * OC + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                tmem_st32(tlane + half * OC + c, reinterpret_cast<uint32_t*>(o));
+              }
+            }
+          }
+          const float neg = m == -INFINITY ? 0.f : -m;
+          uint32_t p[32];
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float x = ex2(fmaf(s[2 * i], sc, neg)), y = ex2(fmaf(s[2 * i + 1], sc, neg));
+            s0 += x;
+            s1 += y;
+            p[i] = pack16<FP8>(x, y);
+          }
+          l += s0 + s1;
+          tmem_st32(ta, p);
+          tmem_wait_st();
+        }
+        if ((it.blk_lo + j + 1) * kKeys > lim0) {
+          // edge tile: clear from V what a zero probability would not silence
+          // A wait on a slot's parity is only sound once the slot's fill before
+          // this one is known to be over: what was loaded ahead of these slots
+          // by a ring's length is K of the next tile or V of the last one.
+          if (j + 1 < n) wait_warp(&sm.s_full[buf ^ 1], ((g + j + 1) >> 1) & 1, abort_flag, a.status);
+          else if (j > 0) wait_warp(&sm.pv_done[buf ^ 1], ((g + j - 1) >> 1) & 1, abort_flag, a.status);
+          const uint32_t vseq = seq + DB * (j + 1 < n ? 2 * j + 2 : 2 * j + 1);
+          const int r = st >> 1;
+          const bool past = (it.blk_lo + j) * kKeys + r >= it.kv;
+          for (int db = 0; db < DB; ++db) {
+            const uint32_t sl = (vseq + db) % C::kSlots, par = ((vseq + db) / C::kSlots) & 1;
+            wait_warp(&sm.full[sl], par, abort_flag, a.status);
+            uint4* v = reinterpret_cast<uint4*>(sm.slot[sl] + r * 128 + (st & 1) * 64);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint4 x = v[c];
+              const uint32_t b0 = nonfinite16<FP8>(x.x), b1 = nonfinite16<FP8>(x.y), b2 = nonfinite16<FP8>(x.z),
+                             b3 = nonfinite16<FP8>(x.w);
+              if (past) {
+                v[c] = make_uint4(0, 0, 0, 0);
+              } else if (b0 | b1 | b2 | b3) {
+                v[c] = make_uint4(x.x & ~b0, x.y & ~b1, x.z & ~b2, x.w & ~b3);
+                sm.poison[item3] = 1;
+              }
+            }
+          }
+          async_fence();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[buf]);
+        prow = prow_next;
+      }
+      // ---- the next item's Q goes in before this item's output goes out
+      g += n;
+      seq = (seq + 2 * DB * n) % (2 * C::kSlots);
+      ++item;
+      const bool have_next = walk.next(a, sm.sched, TPT, kKeys, nx);
+      if (have_next) sc_next = load_q(nx);
+      sm.lx[half][row] = l;
+      const uint32_t mine3 = item3;
+      item3 = item3 == 2 ? 0 : item3 + 1;
+      // the next item's flag: its last readers are past the barrier of the item before this one
+      if (st == 0) sm.poison[item3] = 0;
+      bar_sync(5, 256);
+      l += sm.lx[half ^ 1][row];
+      const bool poison = sm.poison[mine3] != 0;
+      wait_warp(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, a.status);
+      tc_fence_after();
+      if (warp_live) {
+        const size_t orow = (size_t)(it.t0 + tok) * a.Hq + it.kvh * G + (row - tok * G);
+        const size_t prow_out = (size_t)max(it.part, 0) * kRows + row;
+        const float inv = l == 0.f ? 0.f : vmul / l;
+#pragma unroll 1
+        for (int c = 0; c < OC; c += 32) {
+          float o[32];
+          __syncwarp();
+          tmem_ld32(tlane + half * OC + c, o);
+          tmem_wait_ld();
+          if (!live) continue;
+          const int col = half * OC + c;
+          if (l == 0.f) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          }
+          if (poison) {  // non-finite values of the edge tiles that this row sees
+            const int from = max(it.blk_lo, max(lim0, 0) / kKeys) * kKeys, to = min(lim, it.blk_hi * kKeys);
+            for (int t = from; t < to; ++t) {
+              const int pr = page_row(a, pt, t / kPageTokens, n_pages, false);
+              if (pr >= a.num_pages * kPageTokens) continue;
+              const size_t src = ((size_t)(pr + t % kPageTokens) * a.Hkv + it.kvh) * D + col;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float v;
+                if constexpr (FP8) v = Elem<__nv_fp8_e4m3>::get(reinterpret_cast<const __nv_fp8_e4m3*>(a.v_pages), src + i);
+                else v = Elem<__nv_bfloat16>::get(reinterpret_cast<const __nv_bfloat16*>(a.v_pages), src + i);
+                if (!isfinite(v)) o[i] += v;
+              }
+            }
+          }
+          if (it.part < 0) {
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * D + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack16<false>(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                  pack16<false>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                  pack16<false>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                  pack16<false>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(ws.o + prow_out * D + col);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (live && half == 0) {
+          if (it.part >= 0) ws.ml[prow_out] = make_float2(m, l);
+          else if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+        }
+      }
+      if (it.n_parts > 0 && st == 0) ws.desc[blockIdx.x] = ChunkDesc{it.n_parts, it.t0, it.ntok, it.kvh};
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_free);
+      it = nx;
+      have = have_next;
+    }
+  } else if (FP8 && warp >= 12) {
+    // ---------------- codes to FP16 ----------------
+    const int ct = threadIdx.x - 384;                  // 0 .. 127
+    uint32_t r = 0, rphase = 0;
+    while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
+      const int total = 2 * DB * (it.blk_hi - it.blk_lo);
+      for (int i = 0; ok && i < total; ++i) {
+        ok = wait_warp(&sm.raw_full[r], rphase, abort_flag, a.status) &&
+             wait_warp(&sm.empty[s], phase ^ 1, abort_flag, a.status);
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int idx = k * 128 + ct, tr = idx >> 2, c = idx & 3;
+          const uint4 x = *reinterpret_cast<const uint4*>(sm.raw[C::kRaw ? r : 0] + idx * 16);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] & 0xffffu), __NV_E4M3);
+            const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] >> 16), __NV_E4M3);
+            h[2 * e] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
+            h[2 * e + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
+          }
+          unsigned char* dst = sm.slot[s] + tr * 128;
+          *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (tr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (tr & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        async_fence();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.full[s]);
+          mbar_arrive(&sm.raw_empty[r]);
+        }
+        if (++s == C::kSlots) s = 0, phase ^= 1;
+        if (++r == (uint32_t)C::kRaw) r = 0, rphase ^= 1;
+      }
+    }
+  }
+
+  // ---- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {   // nothing may still be in flight when the CTA leaves
+    if (threadIdx.x == 0) {
+      // slots below s were last armed in this round, the others in the one before
+      for (int i = 0; i < (FP8 ? C::kRaw : C::kSlots); ++i)
+        mbar_drain(FP8 ? &sm.raw_full[i] : &sm.full[i], i < (int)s ? phase : phase ^ 1);
+    } else if (threadIdx.x == 32 && issued) {
+      umma::commit(&sm.drain);
+      mbar_drain(&sm.drain, 0);
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  }
+}
+
+// 3-D map over a cache seen as [token rows, Hkv, D]: boxes of 64 columns of
+// one head of a page's 64 tokens.
+bool make_cache_map(CUtensorMap* m, const void* base, const ChunkArgs& a, bool fp8) {
+  umma::EncodeTiledFn fn = umma::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t e = fp8 ? 1 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages * kPageTokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.D * e, (cuuint64_t)a.D * a.Hkv * e};
+  const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kPageTokens};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool FP8>
+cudaError_t launch(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk, float vmul, cudaStream_t s) {
+  CUtensorMap mk, mv;
+  if (!make_cache_map(&mk, a.k_pages, a, FP8) || !make_cache_map(&mv, a.v_pages, a, FP8)) return cudaErrorInvalidValue;
+  auto kern = chunk_tc_kernel<D, FP8>;
+  constexpr size_t smem = sizeof(TcSmem<D, FP8>) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, dim3(grid), dim3(Cfg<D, FP8>::kThreads), smem, s, 1, a, ws, qk, vmul, mk, mv);
+}
+template <int D>
+cudaError_t launch_kv(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk, float vmul, cudaStream_t s) {
+  return a.kv_dt == QSA_FP8_E4M3 ? launch<D, true>(a, ws, grid, qk, vmul, s) : launch<D, false>(a, ws, grid, qk, vmul, s);
+}
+
+}  // namespace
+
+bool chunk_tc_supported(const ChunkArgs& a) {
+  return a.q_dt == QSA_BF16 && (a.kv_dt == QSA_BF16 || a.kv_dt == QSA_FP8_E4M3);
+}
+int chunk_tc_rows() { return kRows; }
+cudaError_t launch_chunk_attn_tc(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk, float vmul, cudaStream_t s) {
+  switch (a.D) {
+    case 64: return launch_kv<64>(a, ws, grid, qk, vmul, s);
+    case 128: return launch_kv<128>(a, ws, grid, qk, vmul, s);
+    default: return launch_kv<256>(a, ws, grid, qk, vmul, s);
+  }
+}
+
 }  // namespace qsa
