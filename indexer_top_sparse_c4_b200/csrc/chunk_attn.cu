@@ -18,6 +18,7 @@
 // a row.  It is bound by the FP32 pipes and serves float32 models, whose
 // values the tensor cores would round.
 #include <math.h>
+#include <stdlib.h>
 
 #include "chunk_common.cuh"
 
@@ -26,6 +27,9 @@ namespace qsa {
 // chunk_attn_tc.cu
 bool chunk_tc_supported(const ChunkArgs& a);
 int chunk_tc_rows();
+// chunk_attn_few.cu
+cudaError_t launch_chunk_attn_few(const ChunkArgs& a, const ChunkWs& ws, int rows, int grid, float qk_scale_log2,
+                                  float vmul, cudaStream_t s);
 cudaError_t launch_chunk_attn_tc(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk_scale_log2, float vmul,
                                  cudaStream_t s);
 
@@ -57,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
   pdl_wait();
   pdl_launch_dependents();
   if (tid == 0 && blockIdx.x < kChunkMaxCtas) ws.desc[blockIdx.x].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, kKeys);
+  chunk_sched_build(a, sm.sched, TPT, kKeys, false);
   ChunkWalk walk;
   walk.begin(a, sm.sched);
   const QT* q = reinterpret_cast<const QT*>(a.q);
@@ -289,13 +293,26 @@ cudaError_t launch_simt_kv(const ChunkArgs& a, const ChunkWs& ws, int grid, floa
     default: return launch_simt<D, QT, __nv_fp8_e4m3>(a, ws, grid, qk, vmul, s);
   }
 }
+// Query rows of a tile of the few-rows kernel (8 or 16), or 0: the wide tiles
+// serve better.  The host knows the batch's tokens, not each request's.
+int few_rows(const ChunkArgs& a) {
+  static const char* f = getenv("QSA_FEW");
+  const int G = a.Hq / a.Hkv;
+  const int rows = (a.T + a.B - 1) / a.B * G;   // of an average request
+  if (rows <= 8) return 8;
+  if (f) return rows <= atoi(f) ? 16 : 0;
+  return rows <= 16 ? 16 : 0;
+}
+
 template <int D>
 cudaError_t launch_d(const ChunkArgs& a, void* wsp, int grid, float qk, float vmul, cudaStream_t s) {
   const bool tc = chunk_tc_supported(a);
-  const int rows = tc ? chunk_tc_rows() : kRows;
+  const int few = tc ? few_rows(a) : 0;
+  const int rows = few ? few : tc ? chunk_tc_rows() : kRows;
   const ChunkWs ws = chunk_ws(wsp, rows, D);
   cudaError_t e;
-  if (tc) e = launch_chunk_attn_tc(a, ws, grid, qk, vmul, s);
+  if (few) e = launch_chunk_attn_few(a, ws, few, grid, qk, vmul, s);
+  else if (tc) e = launch_chunk_attn_tc(a, ws, grid, qk, vmul, s);
   else if (a.q_dt == QSA_F32) e = launch_simt_kv<D, float>(a, ws, grid, qk, vmul, s);
   else e = launch_simt_kv<D, __nv_bfloat16>(a, ws, grid, qk, vmul, s);
   if (e != cudaSuccess) return e;

@@ -194,6 +194,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   using C = Cfg<D, FP8>;
   constexpr int DB = C::DB;
   static_assert(2 * C::kSlots >= 3 * DB, "see the edge tiles");
+  // FP16 P is kept 2^7 larger, so that small probabilities stay in the type's
+  // normal range down to 2^-21 of the largest
+  constexpr float kShift = FP8 ? 7.f : 0.f;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   TcSmem<D, FP8>& sm = *reinterpret_cast<TcSmem<D, FP8>*>(smem_raw + ((1024 - ((uintptr_t)smem_raw & 1023)) & 1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) ws.desc[blockIdx.x].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, kKeys);
+  chunk_sched_build(a, sm.sched, TPT, kKeys, false);
   ChunkWalk walk;
   walk.begin(a, sm.sched);
   ChunkItem it;
@@ -432,9 +435,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           bar_sync(1 + quarter, 64);
           mx = fmaxf(mx, sm.mx[buf][half ^ 1][row]) * sc;
           // move the reference where the maximum has outgrown it
-          const bool grow = mx > m + kGrow || (m == -INFINITY && mx > m);
+          const bool grow = mx > m + (kGrow + kShift) || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, grow)) {
-            const float mn = fmaxf(m, mx);
+            const float mn = fmaxf(m, mx - kShift);
             const float alpha = m == mn ? 1.f : ex2(m - mn);
             m = mn;
             l *= alpha;
@@ -632,26 +635,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   }
 }
 
-// 3-D map over a cache seen as [token rows, Hkv, D]: boxes of 64 columns of
-// one head of a page's 64 tokens.
-bool make_cache_map(CUtensorMap* m, const void* base, const ChunkArgs& a, bool fp8) {
-  umma::EncodeTiledFn fn = umma::encode_fn();
-  if (!fn) return false;
-  const cuuint64_t e = fp8 ? 1 : 2;
-  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages * kPageTokens};
-  const cuuint64_t strides[2] = {(cuuint64_t)a.D * e, (cuuint64_t)a.D * a.Hkv * e};
-  const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kPageTokens};
-  const cuuint32_t estr[3] = {1u, 1u, 1u};
-  return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool FP8>
 cudaError_t launch(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk, float vmul, cudaStream_t s) {
   CUtensorMap mk, mv;
-  if (!make_cache_map(&mk, a.k_pages, a, FP8) || !make_cache_map(&mv, a.v_pages, a, FP8)) return cudaErrorInvalidValue;
+  if (!chunk_cache_map(&mk, a.k_pages, a, FP8, 64, kPageTokens, FP8 ? 0 : 128) ||
+      !chunk_cache_map(&mv, a.v_pages, a, FP8, 64, kPageTokens, FP8 ? 0 : 128))
+    return cudaErrorInvalidValue;
   auto kern = chunk_tc_kernel<D, FP8>;
   constexpr size_t smem = sizeof(TcSmem<D, FP8>) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");

@@ -2,7 +2,7 @@
 // reading of a request's lengths, the cut of the work into tiles of query rows
 // and blocks of keys, and each CTA's share of it.
 #pragma once
-#include "qsa_internal.cuh"
+#include "umma.cuh"
 
 namespace qsa {
 
@@ -98,8 +98,9 @@ __device__ __forceinline__ int chunk_find(const int* v, int n, int x) {
   return lo;
 }
 
-// Called by every thread of the CTA; the table is ready on return.
-__device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched& s, int TPT, int KT) {
+// Called by every thread of the CTA; the table is ready on return.  share: tiles
+// are split over CTAs however many there are (as far as the table holds them).
+__device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched& s, int TPT, int KT, bool share) {
   int carry = 0;
   for (int base = 0; base < a.B; base += blockDim.x) {
     const int b = base + threadIdx.x;
@@ -111,7 +112,7 @@ __device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched
   if (threadIdx.x == 0) {
     s.first[a.B] = carry;
     s.nq = carry;
-    s.shared_tiles = carry <= kChunkMaxTiles && (long long)carry * a.Hkv < 4ll * gridDim.x;
+    s.shared_tiles = carry <= kChunkMaxTiles && (share || (long long)carry * a.Hkv < 4ll * gridDim.x);
   }
   __syncthreads();
   if (s.shared_tiles) {
@@ -210,6 +211,24 @@ __host__ __device__ __forceinline__ ChunkWs chunk_ws(void* ws, int rows, int D) 
   w.ml = reinterpret_cast<float2*>(w.o + (size_t)2 * kChunkMaxCtas * rows * D);
   w.desc = reinterpret_cast<ChunkDesc*>(w.ml + (size_t)2 * kChunkMaxCtas * rows);
   return w;
+}
+
+// 3-D map over a cache seen as [token rows, Hkv, D]: boxes of `cols` values of
+// one head of `rows` tokens, swizzled over 128 or 64 bytes or (0) not at all.
+inline bool chunk_cache_map(CUtensorMap* m, const void* base, const ChunkArgs& a, bool fp8, int cols, int rows,
+                            int swizzle) {
+  umma::EncodeTiledFn fn = umma::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t e = fp8 ? 1 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages * kPageTokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.D * e, (cuuint64_t)a.D * a.Hkv * e};
+  const cuuint32_t box[3] = {(cuuint32_t)cols, 1u, (cuuint32_t)rows};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                           : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace qsa

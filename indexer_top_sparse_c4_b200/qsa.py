@@ -473,27 +473,65 @@ def qsa_dcp_merge_attn(o_parts, lse_parts, out, lse=None, stream=None):
 
 
 # ---- a dense chunk step: tables, rotary and cache write, attention --------------------
+#
+# These calls run many times a step on small inputs, where the time to issue
+# them is the time they take: the checks below read each property of a tensor
+# once, hand plain integers to ctypes and ask for the raw stream.
 
-def _same_device(anchor, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != anchor.device:
-            raise ValueError(f"{name} is on {t.device}, the call runs on {anchor.device}")
-
-
-def _int32(**tensors):
-    for name, t in tensors.items():
-        if t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32 (got {t.dtype})")
+def _device(anchor) -> int:
+    if not anchor.is_cuda:
+        raise ValueError("the tensors must be on a CUDA device")
+    return anchor.get_device()
 
 
-def _call(fn, anchor, stream, *args):
+def _pointers(dev, names, tensors):
+    """Addresses of contiguous tensors on device dev (None stays None)."""
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{names.split()[len(out)]} is on {t.device}, the call runs on cuda:{dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{names.split()[len(out)]}: libqsa takes contiguous tensors")
+        out.append(t.data_ptr())
+    return out
+
+
+_i32 = torch.int32
+
+
+def _int32(names, tensors):
+    for i, t in enumerate(tensors):
+        if t.dtype is not _i32:
+            raise TypeError(f"{names.split()[i]} must be int32 (got {t.dtype})")
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_DTYPES = {torch.float32: QSA_F32, torch.bfloat16: QSA_BF16, torch.float8_e4m3fn: QSA_FP8_E4M3,
+           torch.uint8: QSA_FP8_E4M3}
+
+
+def _code(t: torch.Tensor) -> int:
+    c = _DTYPES.get(t.dtype)
+    if c is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return c
+
+
+def _call(fn, dev, stream, *args):
     """One library call on the device of its tensors, whichever is current;
     stream None: that device's current stream."""
-    if anchor.is_cuda and anchor.device.index != torch.cuda.current_device():
-        with torch.cuda.device(anchor.device):
-            _check(fn(*args, _stream(stream)))
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, s)
     else:
-        _check(fn(*args, _stream(stream)))
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status:
+        _check(status)
 
 
 def qsa_chunk_plan(n_cached, n_new, free_pages, page_table, num_pages, cu_new, kv_len, q_req, q_pos, slot, n_taken,
@@ -502,34 +540,39 @@ def qsa_chunk_plan(n_cached, n_new, free_pages, page_table, num_pages, cu_new, k
     tensors int32; T = the size of q_req, q_pos and slot).  Fills cu_new
     [B + 1], kv_len [B], q_req / q_pos / slot [T] (-1 behind the last token),
     n_taken [1] and the new entries of page_table."""
+    names = "n_cached n_new free_pages page_table cu_new kv_len q_req q_pos slot n_taken dev_status"
+    tensors = (n_cached, n_new, free_pages, page_table, cu_new, kv_len, q_req, q_pos, slot, n_taken)
     B, T = n_cached.numel(), slot.numel()
-    _int32(n_cached=n_cached, n_new=n_new, free_pages=free_pages, page_table=page_table, cu_new=cu_new, kv_len=kv_len,
-           q_req=q_req, q_pos=q_pos, slot=slot, n_taken=n_taken)
-    _same_device(page_table, n_cached=n_cached, n_new=n_new, free_pages=free_pages, cu_new=cu_new, kv_len=kv_len,
-                 q_req=q_req, q_pos=q_pos, slot=slot, n_taken=n_taken, dev_status=dev_status)
+    _int32(names, tensors)
     if (n_new.numel() != B or kv_len.numel() != B or cu_new.numel() != B + 1 or q_req.numel() != T
             or q_pos.numel() != T or n_taken.numel() < 1 or page_table.dim() != 2):
         raise ValueError("shapes: n_cached, n_new, kv_len [B], cu_new [B + 1], q_req, q_pos, slot [T], n_taken [1], "
                          "page_table [pt_rows, pt_stride]")
-    _call(lib().qsa_chunk_plan, page_table, stream, _ptr(n_cached), _ptr(n_new), B, _ptr(free_pages),
-          free_pages.numel(), _ptr(page_table), page_table.shape[0], page_table.shape[1], int(num_pages), T, _ptr(cu_new),
-          _ptr(kv_len), _ptr(q_req), _ptr(q_pos), _ptr(slot), _ptr(n_taken), _ptr(dev_status))
+    dev = _device(page_table)
+    p = _pointers(dev, names, (*tensors, dev_status))
+    rows, width = page_table.shape
+    _call(lib().qsa_chunk_plan, dev, stream, p[0], p[1], B, p[2], free_pages.numel(), p[3], rows, width, int(num_pages),
+          T, *p[4:])
     return cu_new, kv_len, q_req, q_pos, slot, n_taken
 
 
-def _rows(name, x, T, H, D):
+def _rows(dev, name, x, T, H, D):
     """(pointer, row stride) of x [T, H, D] whose rows may be strided."""
-    if tuple(x.shape) != (T, H, D):
+    if x.shape != (T, H, D):
         raise ValueError(f"{name} must be [{T}, {H}, {D}] (got {list(x.shape)})")
-    if x.stride(2) != 1 or (H > 1 and x.stride(1) != D):
+    s0, s1, s2 = x.stride()
+    if s2 != 1 or (H > 1 and s1 != D):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return ctypes.c_void_p(x.data_ptr()), (x.stride(0) if T > 1 else H * D)
+    if x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, the call runs on cuda:{dev}")
+    return x.data_ptr(), (s0 if T > 1 else H * D)
 
 
 def _cache_shape(k_pages, v_pages, Hkv, D):
-    if (k_pages.dim() != 4 or tuple(k_pages.shape[1:]) != (64, Hkv, D) or k_pages.shape != v_pages.shape
-            or k_pages.dtype != v_pages.dtype):
+    shape = k_pages.shape
+    if (len(shape) != 4 or shape[1:] != (64, Hkv, D) or shape != v_pages.shape or k_pages.dtype != v_pages.dtype):
         raise ValueError(f"k_pages and v_pages must be [num_pages, 64, {Hkv}, {D}] of one dtype")
+    return shape[0]
 
 
 def qsa_rope_write(q, k, v, pos, inv_freq, slot, q_out, k_pages, v_pages, sections=None, interleaved_axes=False,
@@ -541,34 +584,38 @@ def qsa_rope_write(q, k, v, pos, inv_freq, slot, q_out, k_pages, v_pages, sectio
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     half = inv_freq.numel()
-    axes = 1 if pos.dim() == 1 else pos.shape[0]
-    sec = [int(n) for n in (sections if sections is not None else (half,))]
+    ps = pos.shape
+    axes = 1 if len(ps) == 1 else ps[0]
     if axes > 1 and sections is None:
         raise ValueError("several axes need their sections")
-    sec += [0] * (3 - len(sec))
+    sec = (half, 0, 0) if sections is None else (*sections, *(0,) * (3 - len(sections)))
     if len(sec) != 3 or not 1 <= axes <= 3:
         raise ValueError("one to three axes and sections")
-    _int32(pos=pos, slot=slot)
-    if pos.shape[-1] != T or slot.numel() != T or pos.dim() > 2:
+    _int32("pos slot", (pos, slot))
+    if ps[-1] != T or slot.numel() != T or len(ps) > 2:
         raise ValueError(f"pos must be [{T}] or [n_axes, {T}], slot [{T}]")
     if T > 1 and pos.stride(-1) != 1:
         raise ValueError("the positions of an axis must be contiguous")
-    if inv_freq.dtype != torch.float32:
+    if inv_freq.dtype is not torch.float32:
         raise TypeError("inv_freq must be float32")
-    if not (q.dtype == k.dtype == v.dtype == q_out.dtype):
+    if not (q.dtype is k.dtype is v.dtype is q_out.dtype):
         raise TypeError("q, k, v and q_out must have one dtype")
-    if tuple(q_out.shape) != (T, Hq, D):
+    if q_out.shape != q.shape:
         raise ValueError("q_out must have q's shape")
-    _cache_shape(k_pages, v_pages, Hkv, D)
-    _same_device(k_pages, q=q, k=k, v=v, pos=pos, inv_freq=inv_freq, slot=slot, q_out=q_out, v_pages=v_pages,
-                 dev_status=dev_status)
-    qp, qs = _rows("q", q, T, Hq, D)
-    kp, ks = _rows("k", k, T, Hkv, D)
-    vp, vs = _rows("v", v, T, Hkv, D)
-    _call(lib().qsa_rope_write, k_pages, stream, qp, qs, kp, ks, vp, vs, _dt(q), ctypes.c_void_p(pos.data_ptr()), axes,
-          pos.stride(0) if axes > 1 else T, *sec, int(bool(interleaved_axes)), int(bool(adjacent_pairs)),
-          _ptr(inv_freq), 2 * half, float(rot_scale), _ptr(slot), T, Hq, Hkv, D, _ptr(q_out), _ptr(k_pages),
-          _ptr(v_pages), _dt(k_pages), float(k_scale), float(v_scale), k_pages.shape[0], _ptr(dev_status))
+    num_pages = _cache_shape(k_pages, v_pages, Hkv, D)
+    x_dt, kv_dt = _code(q), _code(k_pages)
+    dev = k_pages.get_device()
+    qp, qs = _rows(dev, "q", q, T, Hq, D)
+    kp, ks = _rows(dev, "k", k, T, Hkv, D)
+    vp, vs = _rows(dev, "v", v, T, Hkv, D)
+    _device(k_pages)
+    if pos.get_device() != dev:
+        raise ValueError(f"pos is on {pos.device}, the call runs on cuda:{dev}")
+    freq_p, slot_p, out_p, k_p, v_p, st_p = _pointers(dev, "inv_freq slot q_out k_pages v_pages dev_status",
+                                                      (inv_freq, slot, q_out, k_pages, v_pages, dev_status))
+    _call(lib().qsa_rope_write, dev, stream, qp, qs, kp, ks, vp, vs, x_dt, pos.data_ptr(), axes,
+          pos.stride(0) if axes > 1 else T, *sec, 1 if interleaved_axes else 0, 1 if adjacent_pairs else 0, freq_p,
+          2 * half, rot_scale, slot_p, T, Hq, Hkv, D, out_p, k_p, v_p, kv_dt, k_scale, v_scale, num_pages, st_p)
     return q_out
 
 
@@ -586,22 +633,24 @@ def qsa_chunk_attn(q, k_pages, v_pages, page_table, cu_new, kv_len, out, workspa
     cu_new[b+1] - 1 of q [T, Hq, D]) over its kv_len[b] cached tokens."""
     T, Hq, D = q.shape
     B = kv_len.numel()
-    _int32(page_table=page_table, cu_new=cu_new, kv_len=kv_len)
+    _int32("page_table cu_new kv_len", (page_table, cu_new, kv_len))
     if k_pages.dim() != 4:
         raise ValueError("k_pages and v_pages must be [num_pages, 64, Hkv, D]")
     Hkv = k_pages.shape[2]
-    _cache_shape(k_pages, v_pages, Hkv, D)
+    num_pages = _cache_shape(k_pages, v_pages, Hkv, D)
     if cu_new.numel() != B + 1 or page_table.dim() != 2:
         raise ValueError("shapes: kv_len [B], cu_new [B + 1], page_table [pt_rows, pt_stride]")
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError("out must have q's shape and dtype")
-    if lse is not None and (tuple(lse.shape) != (T, Hq) or lse.dtype != torch.float32):
+    if lse is not None and (lse.shape != (T, Hq) or lse.dtype is not torch.float32):
         raise ValueError("lse must be float32 [T, Hq]")
-    _same_device(q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, cu_new=cu_new, kv_len=kv_len, out=out,
-                 workspace=workspace, lse=lse, dev_status=dev_status)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(lib().qsa_chunk_attn, q, stream, _ptr(q), _dt(q), _ptr(k_pages), _ptr(v_pages), _dt(k_pages), float(k_scale),
-          float(v_scale), k_pages.shape[0], _ptr(page_table), page_table.shape[0], page_table.shape[1], _ptr(cu_new),
-          _ptr(kv_len), B, T, Hq, Hkv, D, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
-          _ptr(dev_status))
+    q_dt, kv_dt = _code(q), _code(k_pages)
+    dev = _device(q)
+    q_p, k_p, v_p, pt_p, cu_p, kv_p, out_p, lse_p, ws_p, st_p = _pointers(
+        dev, "q k_pages v_pages page_table cu_new kv_len out lse workspace dev_status",
+        (q, k_pages, v_pages, page_table, cu_new, kv_len, out, lse, workspace, dev_status))
+    rows, width = page_table.shape
+    _call(lib().qsa_chunk_attn, dev, stream, q_p, q_dt, k_p, v_p, kv_dt, k_scale, v_scale, num_pages, pt_p, rows, width,
+          cu_p, kv_p, B, T, Hq, Hkv, D, sm_scale, out_p, lse_p, ws_p,
+          0 if workspace is None else workspace.numel() * workspace.element_size(), st_p)
     return out

@@ -269,3 +269,99 @@ def test_chunk_attention_equals_the_dense_rows_of_the_sparse_path(q):
     # both round the probabilities (2^-8) and the output (2^-8) to bf16
     _, _, tol, _ = b.reference()
     assert bool(((out.double() - b.out.double()).abs() <= 2 * tol).all())
+
+
+# ---- requests of a few rows: the kernel of decode steps and drafts -----------------
+
+DRAFTS = [(0, 1), (1, 2), (15, 1), (14, 2), (16, 1), (63, 2), (200, 2), (0, 0), (1000, 1), (30, 2), (5, 1), (4095, 2)]
+
+
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS)
+@pytest.mark.parametrize("Hq, Hkv, D", [(16, 2, 256), (8, 1, 128), (24, 2, 256), (16, 1, 64), (3, 1, 256), (6, 2, 128),
+                                        (4, 4, 64), (1, 1, 128), (5, 5, 256)])
+def test_drafts(q, Hq, Hkv, D, q_dt, kv_dt):
+    """One and two tokens a request, padded: every tile height and head group."""
+    _run(q, DRAFTS, Hq, Hkv, D, q_dt, kv_dt, seed=20 + D + Hq, pad=2)
+    _run(q, [(n, 1) for n, _ in DRAFTS], Hq, Hkv, D, q_dt, kv_dt, seed=21 + D + Hq)
+
+
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS)
+def test_a_chunk_among_single_tokens(q, q_dt, kv_dt):
+    """Many single tokens and one long chunk: the chunk's tiles are narrow ones."""
+    _run(q, [(i * 13, 1) for i in range(150)] + [(70, 151)], 8, 2, 128, q_dt, kv_dt, seed=22)
+
+
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS)
+@pytest.mark.parametrize("D", [64, 256])
+def test_drafts_hidden_values_and_bad_pages(q, D, q_dt, kv_dt):
+    """NaN in the last token's value reaches that token's row only; a NaN key
+    likewise; pages out of range are skipped and reported."""
+    b = Batch([(300, 2), (77, 2), (500, 1)], 4, 1, D, q_dt, kv_dt, seed=23)
+    for r, what in ((0, b.v), (1, b.k)):
+        p = int(b.kv_len[r]) - 1
+        page, row = int(b.table[r, p // 64]), p % 64
+        if kv_dt == "fp8":
+            what.view(torch.uint8)[page, row, 0, 3] = 0x7f
+        else:
+            what[page, row, 0, 3] = math.nan if r else math.inf
+    b.run(q)
+    b.check()
+    assert bool(torch.isfinite(b.out[[0, 2, 4]].float()).all())
+    good = b.table.clone()
+    b.table[0, 2], b.table[2, 0], b.table[2, 7] = -1, b.num_pages, 2 ** 31 - 1
+    b.run(q)
+    torch.cuda.synchronize()
+    assert int(b.status.item()) == q.QSA_DEV_BAD_PAGE
+    b.table.copy_(good)
+    b.check(status=q.QSA_DEV_BAD_PAGE, skip=((0, 2), (2, 0), (2, 7)))
+
+
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS)
+def test_drafts_sharp_logits_and_row_sizes(q, q_dt, kv_dt):
+    b = Batch([(3000, 2), (60, 2), (9, 1)], 8, 2, 128, q_dt, kv_dt, seed=24)
+    b.q.mul_(8)
+    b.run(q)
+    b.check()
+    b.q.copy_((b.q.float() * torch.exp2(torch.tensor([-60., 3., -20., 0., 9.], device="cuda"))[:, None, None]).to(b.q.dtype))
+    b.q[3] = 0
+    b.run(q)
+    b.check()
+
+
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS)
+def test_one_key_above_a_long_tail(q, q_dt, kv_dt):
+    """One token far above 60,000 equal ones whose probabilities are tiny each
+    and a good part of the output together."""
+    b = Batch([(60000, 1)], 2, 1, 128, q_dt, kv_dt, seed=25)
+    b.q.zero_()
+    b.q[:, :, 0] = 8.0
+    top = float(1.0 / b.k_scale) if kv_dt == "fp8" else 1.0
+    b.k.view(torch.uint8).zero_() if kv_dt == "fp8" else b.k.zero_()
+    page, row = int(b.table[0, 100]), 17
+    b.k[page, row, 0, 0] = torch.tensor(min(15.6 * top, 448.0)).to(b.k.dtype)   # about 11 above the rest
+    b.v.copy_((b.v.float().abs()).to(b.v.dtype))
+    b.run(q)
+    b.check()
+
+
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS[:2])
+def test_drafts_captured_and_repeated(q, q_dt, kv_dt):
+    b = Batch([(5000, 1), (333, 2), (0, 1)], 16, 2, 256, q_dt, kv_dt, seed=26, pad=1)
+    ws = b.workspace(q)
+    b.run(q, workspace=ws)
+    b.check()
+    first, flse = b.out.clone(), b.lse.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        b.run(q, workspace=ws)
+    for kv in ([5001, 335, 1], [17, 2, 1], [3000, 200, 0]):
+        b.kv_len.copy_(torch.tensor(kv, dtype=torch.int32))
+        b.out.fill_(7.0)
+        b.lse.fill_(7.0)
+        torch.cuda.synchronize()
+        g.replay()
+        b.check()
+        if kv[0] == 5001:
+            assert torch.equal(first, b.out) and torch.equal(flse, b.lse)
