@@ -18,7 +18,6 @@
 // a row.  It is bound by the FP32 pipes and serves float32 models, whose
 // values the tensor cores would round.
 #include <math.h>
-#include <stdlib.h>
 
 #include "chunk_common.cuh"
 
@@ -61,9 +60,9 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
   pdl_wait();
   pdl_launch_dependents();
   if (tid == 0 && blockIdx.x < kChunkMaxCtas) ws.desc[blockIdx.x].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, kKeys, false);
+  chunk_sched_build(a, sm.sched, TPT, kKeys, gridDim.x, false);
   ChunkWalk walk;
-  walk.begin(a, sm.sched);
+  walk.begin(a, sm.sched, blockIdx.x, gridDim.x);
   const QT* q = reinterpret_cast<const QT*>(a.q);
   const KVT* kc = reinterpret_cast<const KVT*>(a.k_pages);
   const KVT* vc = reinterpret_cast<const KVT*>(a.v_pages);
@@ -296,11 +295,9 @@ cudaError_t launch_simt_kv(const ChunkArgs& a, const ChunkWs& ws, int grid, floa
 // Query rows of a tile of the few-rows kernel (8 or 16), or 0: the wide tiles
 // serve better.  The host knows the batch's tokens, not each request's.
 int few_rows(const ChunkArgs& a) {
-  static const char* f = getenv("QSA_FEW");
   const int G = a.Hq / a.Hkv;
   const int rows = (a.T + a.B - 1) / a.B * G;   // of an average request
   if (rows <= 8) return 8;
-  if (f) return rows <= atoi(f) ? 16 : 0;
   return rows <= 16 ? 16 : 0;
 }
 
@@ -309,7 +306,7 @@ cudaError_t launch_d(const ChunkArgs& a, void* wsp, int grid, float qk, float vm
   const bool tc = chunk_tc_supported(a);
   const int few = tc ? few_rows(a) : 0;
   const int rows = few ? few : tc ? chunk_tc_rows() : kRows;
-  const ChunkWs ws = chunk_ws(wsp, rows, D);
+  const ChunkWs ws = chunk_ws(wsp, D);
   cudaError_t e;
   if (few) e = launch_chunk_attn_few(a, ws, few, grid, qk, vmul, s);
   else if (tc) e = launch_chunk_attn_tc(a, ws, grid, qk, vmul, s);
@@ -317,7 +314,8 @@ cudaError_t launch_d(const ChunkArgs& a, void* wsp, int grid, float qk, float vm
   else e = launch_simt_kv<D, __nv_bfloat16>(a, ws, grid, qk, vmul, s);
   if (e != cudaSuccess) return e;
   auto comb = a.q_dt == QSA_F32 ? chunk_combine_kernel<D, float> : chunk_combine_kernel<D, __nv_bfloat16>;
-  return launch_k(comb, dim3(grid, kCombineY), dim3(kCombineThreads), 0, s, 1, a, ws, rows, vmul);
+  const int workers = tc && !few ? grid / 2 : grid;   // who may have opened a tile that others finish
+  return launch_k(comb, dim3(workers, kCombineY), dim3(kCombineThreads), 0, s, 1, a, ws, rows, vmul);
 }
 
 }  // namespace
@@ -326,7 +324,7 @@ int chunk_attn_max_requests() { return kChunkMaxReq; }
 
 size_t chunk_attn_ws_bytes(int T, int B, int Hq, int Hkv, int D, qsa_dtype_t kv_dt) {
   (void)T, (void)B, (void)Hq, (void)Hkv, (void)kv_dt;
-  return chunk_ws_bytes(chunk_tc_rows() > kRows ? chunk_tc_rows() : kRows, D);
+  return chunk_ws_bytes(D);
 }
 
 cudaError_t launch_chunk_attn(const ChunkArgs& a, void* ws, cudaStream_t s) {

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) ws.desc[blockIdx.x].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, KT, true);
+  chunk_sched_build(a, sm.sched, TPT, KT, gridDim.x, true);
 
   // Keys this tile's last row sees, and the steps of a piece that hold any.
   auto steps_of = [&](const ChunkItem& x) {
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
 
   // ---- the load stream: K and V of this warp's steps, piece after piece
   ChunkWalk lwalk;
-  lwalk.begin(a, sm.sched);
+  lwalk.begin(a, sm.sched, blockIdx.x, gridDim.x);
   ChunkItem lit;
   int ls = 0, lns = 0, lwin = -1, lpage = 0, ly = 0;
   uint32_t issued = 0, badmask = 0;   // slots armed; by slot: a bad page
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
 
   // ---- the pieces
   ChunkWalk walk;
-  walk.begin(a, sm.sched);
+  walk.begin(a, sm.sched, blockIdx.x, gridDim.x);
   ChunkItem it;
   uint32_t slot = 0, phase = 0, parity = 0;
   auto wait_slot = [&]() {

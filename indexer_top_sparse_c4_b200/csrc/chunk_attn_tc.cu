@@ -10,23 +10,28 @@
 // it, which keeps P in range of its 16-bit type and leaves O in TMEM alone in
 // almost every step.
 //
-// sm_100a design, one persistent CTA per SM:
-//  * tile: M = 128 query rows (one TMEM lane each) x N = 128 keys (two pages).
-//    The rows are whole tokens: all G = Hq / Hkv query heads of a KV head, so
-//    a key or value read once serves 128 / G tokens x G heads; a decode step
-//    uses G of the rows and is bound by the cache read.
+// sm_100a design, a persistent pair of CTAs (cluster of 2, cta_group::2) per two
+// SMs:
+//  * tile: M = 256 query rows (128 TMEM lanes in each CTA) x N = 128 keys (two
+//    pages).  The rows are whole tokens: all G = Hq / Hkv query heads of a KV
+//    head, so a key or value read once serves 256 / G tokens x G heads.
+//  * each CTA stages half of the B operands: one page of keys (64 of the 128
+//    columns of S) and half of the head's value columns.  A single CTA per tile
+//    would pull 128 KB from L2 for 2,048 cycles of products at D = 256 and read
+//    320 KB of shared memory (2,560 cycles) for them; the pair halves the
+//    first and needs 1,500 cycles for the second.
 //  * TMEM (512 columns): O in columns 0 .. D-1, two S tiles of 128 columns; P
 //    overwrites its S tile (16-bit, half the columns) and is the A operand of
 //    P V straight from TMEM.
-//  * keys and values stream through one ring of 16 KB slots (128 tokens x 64
-//    columns, 128-byte swizzle): a K tile is D / 64 slots, the K-major B
-//    operand of S; a V tile is D / 64 slots, each the MN-major B operand of 64
-//    columns of O.  Order K0, K1, V0, K2, V1, ...: S of the next tile is
-//    computed while the softmax of this one runs.
-//  * warp 0 issues the TMA loads (one box per page and slot, pages looked up
-//    32 at a time), warp 1 the MMAs, warps 4..11 the softmax (two warps per
-//    TMEM lane quarter, 64 keys each: the two exchange row maxima through
-//    shared memory).
+//  * keys and values stream through one ring of stages (a K or V half tile
+//    each; 32 KB at D = 256), in the order K0, K1, V0, K2, V1, ...: S of the
+//    next tile is computed while the softmax of this one runs.  V is the
+//    MN-major B operand, D columns in one product: products of 64 columns take
+//    52 cycles instead of 32 (measured), those of 256 columns 131 of 128.
+//  * warp 0 issues the CTA's TMA loads (boxes of one page x 64 columns, pages
+//    looked up 32 at a time), warp 1 of the first CTA the MMAs of both; warps
+//    4..11 do the softmax of the CTA's rows (two warps per TMEM lane quarter,
+//    64 keys each).
 //  * FP8 cache: boxes of codes land in a second ring, and warps 12..15 turn
 //    them into FP16 slots (e4m3 is a subset of FP16, the product P V then
 //    takes P in FP16).  The query is FP16 too: each row is scaled by a power
@@ -54,10 +59,8 @@ namespace {
 
 using namespace mbar;
 
-constexpr int kRows = 128;
+constexpr int kRows = 128;               // rows of a CTA, half of a tile
 constexpr int kKeys = 128;               // keys of a tile: two pages
-constexpr int kSlotBytes = kKeys * 128;  // 128 tokens x 64 16-bit columns
-constexpr int kRawBytes = kKeys * 64;    // 128 tokens x 64 codes
 constexpr uint32_t kSCol = 256;          // first TMEM column of the S tiles
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSoftWarps = 8;
@@ -66,25 +69,34 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D, bool FP8>
 struct Cfg {
-  static constexpr int DB = D / 64;   // slots of a tile (the edge tiles' waits need 1.5 tiles of ring)
-  // Q + rings take 208 KB: nine BF16 slots at D = 256 (2.25 tiles ahead)
-  static constexpr int kSlots = FP8 ? (D == 256 ? 6 : 8) : (D == 256 ? 9 : D == 128 ? 11 : 12);
-  static constexpr int kRaw = FP8 ? 6 : 0;
-  static constexpr int kThreads = FP8 ? 512 : 384;
+  static constexpr int DB = D / 64;                    // 64-column blocks of a key half: 64 rows of 128 bytes each
+  static constexpr int VB = D >= 128 ? D / 128 : 1;    // column blocks of a value half: 128 rows of VR bytes each
+  static constexpr int VR = D >= 128 ? 128 : 64;
+  static constexpr int kStage = 64 * D * 2;            // a key half or a value half, 16-bit
+  static constexpr int kRaw = 64 * D;                  // the same in codes
   static constexpr int kQBytes = DB * kRows * 128;
+  // Q and the rings take up to 208 KB
+  static constexpr int kStages = FP8 ? (D == 256 ? 3 : 6) : (D == 256 ? 4 : 8);
+  static constexpr int kRaws = FP8 ? (D == 256 ? 3 : 6) : 0;
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  // registers after the split: loads and MMA, softmax, conversion (their sum is within the launch's 3 x 168 or 4 x 128)
+  static constexpr int kRegLow = FP8 ? 64 : 72, kRegSoft = FP8 ? 184 : 216, kRegConv = 80;
 };
 
 template <int D, bool FP8>
 struct TcSmem {
   using C = Cfg<D, FP8>;
   alignas(1024) unsigned char q[C::kQBytes];
-  alignas(1024) unsigned char slot[C::kSlots][kSlotBytes];
-  alignas(1024) unsigned char raw[C::kRaw ? C::kRaw : 1][C::kRaw ? kRawBytes : 16];
-  alignas(8) uint64_t full[C::kSlots], empty[C::kSlots];
+  alignas(1024) unsigned char stage[C::kStages][C::kStage];
+  alignas(1024) unsigned char raw[C::kRaws ? C::kRaws : 1][C::kRaws ? C::kRaw : 16];
+  // Waited for by the first CTA's MMA warp, arrived at from both CTAs: full,
+  // q_full, p_full, o_free.  Signalled in both CTAs by the MMA warp: the others
+  // but raw_*, which are the CTA's own.
   // s_full, p_full and pv_done count tiles, one of each two: a waiter is never
-  // more than one phase ahead of a barrier, so a phase's parity names it
-  uint64_t raw_full[C::kRaw ? C::kRaw : 1], raw_empty[C::kRaw ? C::kRaw : 1];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, drain;
+  // more than one phase ahead of a barrier, so a phase's parity names it.
+  alignas(8) uint64_t full[C::kStages], empty[C::kStages];
+  uint64_t raw_full[C::kRaws ? C::kRaws : 1], raw_empty[C::kRaws ? C::kRaws : 1];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, v_ready, drain;
   float mx[2][2][kRows];                 // [tile parity][half][row] maxima
   float lx[2][kRows];                    // [half][row] sums
   float q_scale[kRows];                  // FP8: what undoes the row's power of two
@@ -100,21 +112,66 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       ::"r"(saddr(dst)), "l"(map), "r"(saddr(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// The same, signalling the barrier at the same place of the pair's first CTA.
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(saddr(dst)), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// Addresses in the pair's CTAs, arrivals there.
+__device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // A and B in shared memory / A in TMEM
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  umma::mma_bf16(d, a, b, idesc, acc);   // kind::f16: the operand type is idesc's
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
       ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
-// kind::f16 instruction descriptor: F32 accumulators, M = 128; f16 or bf16
+// Arrives on the barrier at this place in both CTAs once the MMAs issued before are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(saddr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// MN-major operand of rows of VR bytes: 8-row atoms, column blocks 128 rows apart
+template <int VR>
+__device__ __forceinline__ uint64_t v_desc(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFF);
+  d |= (uint64_t)((128 * VR) >> 4) << 16;        // to the next column block
+  d |= (uint64_t)((8 * VR) >> 4) << 32;          // to the next 8 keys
+  d |= (uint64_t)1 << 46;                        // version
+  d |= (uint64_t)(VR == 128 ? 2 : 4) << 61;      // swizzle over 128 or 64 bytes
+  return d;
+}
+// kind::f16 instruction descriptor: F32 accumulators, M = 256; f16 or bf16
 // operands; B K-major (keys of S) or MN-major (values)
 constexpr uint32_t idesc(bool f16, int N, bool b_mn) {
   return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(kRows >> 4) << 24);
+         ((uint32_t)(2 * kRows >> 4) << 24);
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
   uint32_t* u = reinterpret_cast<uint32_t*>(r);
@@ -161,6 +218,7 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // A wait that gives up at once when the CTA is stopping.
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
   if (*abort_flag) return false;
+  if (mbar_try_wait(b, parity)) return true;
   return mbar_wait(b, parity, abort_flag, status);
 }
 // The same by a whole warp, which is converged on return (the TMEM loads and
@@ -193,7 +251,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                     const __grid_constant__ CUtensorMap map_v) {
   using C = Cfg<D, FP8>;
   constexpr int DB = C::DB;
-  static_assert(2 * C::kSlots >= 3 * DB, "see the edge tiles");
   // FP16 P is kept 2^7 larger, so that small probabilities stay in the type's
   // normal range down to 2^-21 of the largest
   constexpr float kShift = FP8 ? 7.f : 0.f;
@@ -201,159 +258,186 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   TcSmem<D, FP8>& sm = *reinterpret_cast<TcSmem<D, FP8>*>(smem_raw + ((1024 - ((uintptr_t)smem_raw & 1023)) & 1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sm.abort_flag;
-  const int G = a.Hq / a.Hkv, TPT = kRows / G;
+  const int G = a.Hq / a.Hkv, TPT = 2 * kRows / G;
+  const uint32_t rank = cluster_rank();
+  const int worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(&sm.full[s], FP8 ? 4 : 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sm.full[s], FP8 ? 8 : 1);
       mbar_init(&sm.empty[s], 1);
     }
-    for (int s = 0; s < C::kRaw; ++s) {
+    for (int s = 0; s < C::kRaws; ++s) {
       mbar_init(&sm.raw_full[s], 1);
       mbar_init(&sm.raw_empty[s], 4);
     }
-    mbar_init(&sm.q_full, kSoftWarps);
+    mbar_init(&sm.q_full, 2 * kSoftWarps);
     mbar_init(&sm.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.p_full[s], kSoftWarps);
+      mbar_init(&sm.p_full[s], 2 * kSoftWarps);
       mbar_init(&sm.pv_done[s], 1);
     }
-    mbar_init(&sm.o_free, kSoftWarps);
+    mbar_init(&sm.o_free, 2 * kSoftWarps);
+    mbar_init(&sm.v_ready, 1);
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     sm.poison[0] = sm.poison[1] = sm.poison[2] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sm.tmem_base)),
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&sm.tmem_base)),
                  "r"(kTmemCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();          // the pair's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   pdl_wait();
   pdl_launch_dependents();
-  if (threadIdx.x == 0) ws.desc[blockIdx.x].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, kKeys, false);
+  if (threadIdx.x == 0 && rank == 0) ws.desc[worker].n_parts = 0;
+  chunk_sched_build(a, sm.sched, TPT, kKeys, workers, false);
   ChunkWalk walk;
-  walk.begin(a, sm.sched);
+  walk.begin(a, sm.sched, worker, workers);
   ChunkItem it;
   uint32_t s = 0, phase = 0;   // ring position of the loading, issuing and converting warps
   bool ok = true, issued = false;
 
-  if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    constexpr int kRing = FP8 ? C::kRaw : C::kSlots;
-    constexpr uint32_t kBytes = FP8 ? kRawBytes : kSlotBytes;
-    uint64_t* const fulls = FP8 ? sm.raw_full : sm.full;
-    uint64_t* const empties = FP8 ? sm.raw_empty : sm.empty;
-    while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
-      const int n = it.blk_hi - it.blk_lo, lp0 = 2 * it.blk_lo;
-      const int n_pages = (it.kv + kPageTokens - 1) / kPageTokens;
-      const int32_t* pt = a.page_table + (size_t)it.b * a.pt_stride;
-      // rows of pages 32 w .. 32 w + 31 of this piece, and the next 32
-      int win = 0, last_lp = lp0 + 2 * n;
-      int cur = page_row(a, pt, lp0 + lane, min(n_pages, last_lp), true);
-      int nxt = page_row(a, pt, lp0 + 32 + lane, min(n_pages, last_lp), true);
-      auto load_tile = [&](const CUtensorMap* map, int j) {
-        const int x = 2 * j, from = (x >> 5) == win ? cur : nxt;
-        const int y0 = __shfl_sync(0xffffffffu, from, x & 31), y1 = __shfl_sync(0xffffffffu, from, (x + 1) & 31);
-        for (int db = 0; db < DB; ++db) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegLow));
+    if (warp == 0) {
+      // ---------------- TMA producer: this CTA's halves ----------------
+      constexpr int kRing = FP8 ? C::kRaws : C::kStages;
+      constexpr uint32_t kBytes = FP8 ? C::kRaw : C::kStage;
+      uint64_t* const empties = FP8 ? sm.raw_empty : sm.empty;
+      while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
+        const int n = it.blk_hi - it.blk_lo, lp0 = 2 * it.blk_lo;
+        const int n_pages = min((it.kv + kPageTokens - 1) / kPageTokens, lp0 + 2 * n);
+        const int32_t* pt = a.page_table + (size_t)it.b * a.pt_stride;
+        // rows of pages 32 w .. 32 w + 31 of this piece, and the next 32
+        int win = 0;
+        int cur = page_row(a, pt, lp0 + lane, n_pages, rank == 0);
+        int nxt = page_row(a, pt, lp0 + 32 + lane, n_pages, rank == 0);
+        auto load = [&](bool key, int j) {
+          const int x = 2 * j, from = (x >> 5) == win ? cur : nxt;
+          const int y0 = __shfl_sync(0xffffffffu, from, x & 31), y1 = __shfl_sync(0xffffffffu, from, (x + 1) & 31);
           ok = wait_warp(&empties[s], phase ^ 1, abort_flag, a.status);
           if (!ok) return;
           if (lane == 0) {
-            unsigned char* dst = FP8 ? sm.raw[s] : sm.slot[s];
-            mbar_arrive_tx(&fulls[s], kBytes);
-            tma_load_3d(dst, map, &fulls[s], db * 64, it.kvh, y0);
-            tma_load_3d(dst + kBytes / 2, map, &fulls[s], db * 64, it.kvh, y1);
+            uint64_t* const own = &sm.raw_full[FP8 ? s : 0];
+            const uint32_t bar = map_cta(saddr(&sm.full[FP8 ? 0 : s]), 0);
+            unsigned char* dst = FP8 ? sm.raw[s] : sm.stage[s];
+            if (FP8) mbar_arrive_tx(own, kBytes);
+            else if (rank == 0) mbar_arrive_tx(&sm.full[s], 2 * kBytes);   // both CTAs' bytes
+            auto box = [&](uint32_t off, const CUtensorMap* map, int col, int y) {
+              if constexpr (FP8) tma_load_3d(dst + off, map, own, col, it.kvh, y);
+              else tma_load_3d_pair(dst + off, map, bar, col, it.kvh, y);
+            };
+            if (key) {        // page `rank` of the two, all columns
+#pragma unroll
+              for (int db = 0; db < DB; ++db) box(db * (kBytes / DB), &map_k, db * 64, rank ? y1 : y0);
+            } else {          // half of the columns, both pages
+#pragma unroll
+              for (int vb = 0; vb < C::VB; ++vb) {
+                const int col = (int)rank * (D / 2) + vb * 64;
+                box(vb * (kBytes / C::VB), &map_v, col, y0);
+                box(vb * (kBytes / C::VB) + kBytes / C::VB / 2, &map_v, col, y1);
+              }
+            }
           }
+          __syncwarp();
           if (++s == kRing) s = 0, phase ^= 1;
+        };
+        load(true, 0);
+        for (int j = 0; ok && j < n; ++j) {
+          if (j + 1 < n) load(true, j + 1);
+          if (ok) load(false, j);
+          if (((2 * j + 2) >> 5) != win) {   // the next V tile lies in the next window
+            ++win;
+            cur = nxt;
+            nxt = page_row(a, pt, lp0 + 32 * (win + 1) + lane, n_pages, rank == 0);
+          }
         }
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- MMA issuer of the pair ----------------
+      constexpr uint32_t kIdS = idesc(FP8, kKeys, false), kIdO = idesc(FP8, D, true);
+      const uint64_t qd = umma::smem_desc(saddr(sm.q));
+      const uint32_t ready0 = map_cta(saddr(&sm.v_ready), 0), ready1 = map_cta(saddr(&sm.v_ready), 1);
+      uint32_t g = 0, item = 0;
+      auto step = [&]() { if (++s == C::kStages) s = 0, phase ^= 1; };
+      auto qk = [&](uint32_t buf) {
+        ok = ok && wait_warp(&sm.full[s], phase, abort_flag, a.status);
+        if (!ok) return;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint64_t kd = umma::smem_desc(saddr(sm.stage[s]));
+#pragma unroll
+          for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss(tmem + kSCol + buf * kKeys, qd + (db * (kRows * 128) >> 4) + ks * 2,
+                     kd + (db * (64 * 128) >> 4) + ks * 2, kIdS, (db | ks) != 0);
+          commit_pair(&sm.s_full[buf]);
+          commit_pair(&sm.empty[s]);
+          issued = true;
+        }
+        __syncwarp();
+        step();
       };
-      load_tile(&map_k, 0);
-      for (int j = 0; ok && j < n; ++j) {
-        if (j + 1 < n) load_tile(&map_k, j + 1);
-        if (ok) load_tile(&map_v, j);
-        if (((2 * j + 2) >> 5) != win) {   // the next V tile lies in the next window
-          ++win;
-          cur = nxt;
-          nxt = page_row(a, pt, lp0 + 32 * (win + 1) + lane, min(n_pages, last_lp), true);
+      while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
+        const int n = it.blk_hi - it.blk_lo;
+        const int lim0 = min(it.p0 + 1, it.kv);
+        ok = wait_warp(&sm.q_full, item & 1, abort_flag, a.status);
+        if (ok) qk(g & 1);
+        for (int j = 0; ok && j < n; ++j) {
+          const uint32_t buf = (g + j) & 1;
+          if (j + 1 < n) qk(buf ^ 1);
+          if (!ok) break;
+          if (j + 2 >= n && (j + 1 < n || n == 1) && lane == 0) commit_pair(&sm.q_empty);  // after the last Q K^T
+          __syncwarp();
+          // the previous item's O has been read out before the first P V
+          if (j == 0) ok = wait_warp(&sm.o_free, (item & 1) ^ 1, abort_flag, a.status);
+          ok = ok && wait_warp(&sm.full[s], phase, abort_flag, a.status);
+          if (ok && (it.blk_lo + j + 1) * kKeys > lim0) {   // edge tile: the softmax warps clear V first
+            if (lane == 0) arrive_at(ready0), arrive_at(ready1);
+            __syncwarp();
+          }
+          ok = ok && wait_warp(&sm.p_full[buf], ((g + j) >> 1) & 1, abort_flag, a.status);
+          if (!ok) break;
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t vd = v_desc<C::VR>(saddr(sm.stage[s]));
+            const uint32_t p = tmem + kSCol + buf * kKeys;
+            // 16 keys a step: 8 columns of P, 16 rows of V; keys 64.. of P start 64 columns on
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma_ts(tmem, p + (ks >> 2) * 64 + (ks & 3) * 8, vd + ks * (16 * C::VR >> 4), kIdO, j != 0 || ks != 0);
+            commit_pair(&sm.pv_done[buf]);
+            commit_pair(&sm.empty[s]);
+            issued = true;
+          }
+          __syncwarp();
+          step();
         }
+        g += n;
+        ++item;
       }
     }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    constexpr uint32_t kIdS = idesc(FP8, kKeys, false), kIdO = idesc(FP8, 64, true);
-    const uint64_t qd = umma::smem_desc(saddr(sm.q));
-    uint32_t g = 0, item = 0;
-    auto step = [&]() { if (++s == C::kSlots) s = 0, phase ^= 1; };
-    auto qk = [&](uint32_t buf) {
-      for (int db = 0; db < DB; ++db) {
-        ok = ok && wait_warp(&sm.full[s], phase, abort_flag, a.status);
-        if (!ok) return;
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t kd = umma::smem_desc(saddr(sm.slot[s]));
-          const uint64_t qa = qd + (uint64_t)(db * (kRows * 128) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_ss(tmem + kSCol + buf * kKeys, qa + ks * 2, kd + ks * 2, kIdS, (db | ks) != 0);
-          umma::commit(&sm.empty[s]);
-          if (db == DB - 1) umma::commit(&sm.s_full[buf]);
-          issued = true;
-        }
-        __syncwarp();
-        step();
-      }
-    };
-    auto pv = [&](uint32_t buf, bool first) {
-      for (int db = 0; db < DB; ++db) {
-        ok = ok && wait_warp(&sm.full[s], phase, abort_flag, a.status);
-        if (!ok) return;
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t vd = umma::smem_desc(saddr(sm.slot[s]));
-          const uint32_t p = tmem + kSCol + buf * kKeys;
-          // 16 keys a step: 8 columns of P, 16 rows (2 KB) of V; keys 64.. of P start 64 columns on
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ts(tmem + db * 64, p + (ks >> 2) * 64 + (ks & 3) * 8, vd + ks * 128, kIdO, !first || ks != 0);
-          umma::commit(&sm.empty[s]);
-          if (db == DB - 1) umma::commit(&sm.pv_done[buf]);
-          issued = true;
-        }
-        __syncwarp();
-        step();
-      }
-    };
-    while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
-      const int n = it.blk_hi - it.blk_lo;
-      ok = wait_warp(&sm.q_full, item & 1, abort_flag, a.status);
-      if (ok) qk(g & 1);
-      for (int j = 0; ok && j < n; ++j) {
-        if (j + 1 < n) qk((g + j + 1) & 1);
-        if (!ok) break;
-        if (j + 2 >= n && (j + 1 < n || n == 1) && lane == 0) umma::commit(&sm.q_empty);  // after the last Q K^T
-        __syncwarp();
-        // the previous item's O has been read out before the first P V
-        if (j == 0) ok = wait_warp(&sm.o_free, (item & 1) ^ 1, abort_flag, a.status);
-        ok = ok && wait_warp(&sm.p_full[(g + j) & 1], ((g + j) >> 1) & 1, abort_flag, a.status);
-        if (ok) pv((g + j) & 1, j == 0);
-      }
-      g += n;
-      ++item;
-    }
-  } else if (warp >= 4 && warp < 4 + kSoftWarps) {
+  } else if (warp < 4 + kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
     // ---------------- softmax, correction, epilogue ----------------
     const int st = threadIdx.x - 128;                  // 0 .. 255
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int row = 32 * quarter + lane;
     const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
     constexpr int OC = D / 2;                          // columns of O per thread
-    uint32_t g = 0, item = 0, item3 = 0, seq = 0;                 // tiles, items, slots (of two rounds) so far
+    const uint32_t q_full0 = map_cta(saddr(&sm.q_full), 0), o_free0 = map_cta(saddr(&sm.o_free), 0);
+    const uint32_t p_full0 = map_cta(saddr(&sm.p_full[0]), 0);
+    uint32_t g = 0, item = 0, item3 = 0;               // tiles, items so far
+    uint32_t pos = 0, edges = 0;                       // ring stage of the item's first K; edge tiles so far
 
     // Q of the next item into shared memory (128-byte swizzle, K-major); rows
     // past its tokens are zero
@@ -364,10 +448,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       const int rows = x.ntok * G;
 #pragma unroll 4
       for (int i = st; i < kRows * CH; i += 256) {
-        const int r = i / CH, c = i % CH;
+        const int r = i / CH, c = i % CH, tr = (int)rank * kRows + r;
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-          v = *reinterpret_cast<const uint4*>(q + ((size_t)(x.t0 + r / G) * a.Hq + x.kvh * G + r % G) * D + c * 8);
+        if (tr < rows)
+          v = *reinterpret_cast<const uint4*>(q + ((size_t)(x.t0 + tr / G) * a.Hq + x.kvh * G + tr % G) * D + c * 8);
         if constexpr (FP8) {
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
           uint32_t top = 0;                            // the row's largest exponent field
@@ -387,7 +471,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       }
       async_fence();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.q_full);
+      if (lane == 0) arrive_at(q_full0);
       float sc = qk_scale_log2;
       if constexpr (FP8) {
         bar_sync(5, 256);
@@ -402,9 +486,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     while (have) {
       const float sc = sc_next;
       const int n = it.blk_hi - it.blk_lo, rows = it.ntok * G;
-      const int tok = row / G;
-      const bool live = row < rows;                    // this thread's row is a query
-      const bool warp_live = 32 * quarter < rows;
+      const int trow = (int)rank * kRows + row, tok = trow / G;
+      const bool live = trow < rows;                   // this thread's row is a query
+      const bool warp_live = (int)rank * kRows + 32 * quarter < rows;
       const int lim = live ? min(it.p0 + tok + 1, it.kv) : 0;   // keys the row sees
       const int lim0 = min(it.p0 + 1, it.kv);          // keys the tile's first row sees (the fewest)
       const int n_pages = (it.kv + kPageTokens - 1) / kPageTokens;
@@ -471,20 +555,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         }
         if ((it.blk_lo + j + 1) * kKeys > lim0) {
           // edge tile: clear from V what a zero probability would not silence
-          // A wait on a slot's parity is only sound once the slot's fill before
-          // this one is known to be over: what was loaded ahead of these slots
-          // by a ring's length is K of the next tile or V of the last one.
-          if (j + 1 < n) wait_warp(&sm.s_full[buf ^ 1], ((g + j + 1) >> 1) & 1, abort_flag, a.status);
-          else if (j > 0) wait_warp(&sm.pv_done[buf ^ 1], ((g + j - 1) >> 1) & 1, abort_flag, a.status);
-          const uint32_t vseq = seq + DB * (j + 1 < n ? 2 * j + 2 : 2 * j + 1);
+          wait_warp(&sm.v_ready, edges & 1, abort_flag, a.status);
+          ++edges;
+          const uint32_t vs = (pos + (j + 1 < n ? 2 * j + 2 : 2 * j + 1)) % C::kStages;   // K of the next tile goes first
           const int r = st >> 1;
           const bool past = (it.blk_lo + j) * kKeys + r >= it.kv;
-          for (int db = 0; db < DB; ++db) {
-            const uint32_t sl = (vseq + db) % C::kSlots, par = ((vseq + db) / C::kSlots) & 1;
-            wait_warp(&sm.full[sl], par, abort_flag, a.status);
-            uint4* v = reinterpret_cast<uint4*>(sm.slot[sl] + r * 128 + (st & 1) * 64);
+          bool odd = false;
+          for (int vb = 0; vb < C::VB; ++vb) {
+            uint4* v = reinterpret_cast<uint4*>(sm.stage[vs] + vb * (kKeys * C::VR) + r * C::VR + (st & 1) * (C::VR / 2));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < C::VR / 32; ++c) {
               uint4 x = v[c];
               const uint32_t b0 = nonfinite16<FP8>(x.x), b1 = nonfinite16<FP8>(x.y), b2 = nonfinite16<FP8>(x.z),
                              b3 = nonfinite16<FP8>(x.w);
@@ -492,36 +572,45 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                 v[c] = make_uint4(0, 0, 0, 0);
               } else if (b0 | b1 | b2 | b3) {
                 v[c] = make_uint4(x.x & ~b0, x.y & ~b1, x.z & ~b2, x.w & ~b3);
-                sm.poison[item3] = 1;
+                odd = true;
               }
             }
+          }
+          if (odd) {   // both CTAs' rows may see it
+#pragma unroll
+            for (uint32_t cta = 0; cta < 2; ++cta)
+              asm volatile("st.relaxed.cluster.shared::cluster.b32 [%0], %1;" ::"r"(map_cta(saddr(&sm.poison[item3]), cta)),
+                           "r"(1)
+                           : "memory");
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
           }
           async_fence();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[buf]);
+        if (lane == 0) arrive_at(p_full0 + buf * 8);
         prow = prow_next;
       }
       // ---- the next item's Q goes in before this item's output goes out
       g += n;
-      seq = (seq + 2 * DB * n) % (2 * C::kSlots);
+      pos = (pos + 2 * n) % C::kStages;
       ++item;
+      const uint32_t mine3 = item3;
+      item3 = item3 == 2 ? 0 : item3 + 1;
+      // The next item's flag: its last readers are past the barrier of the item
+      // before this one, its writers behind the arrivals for the next Q.
+      if (st == 0) sm.poison[item3] = 0;
       const bool have_next = walk.next(a, sm.sched, TPT, kKeys, nx);
       if (have_next) sc_next = load_q(nx);
       sm.lx[half][row] = l;
-      const uint32_t mine3 = item3;
-      item3 = item3 == 2 ? 0 : item3 + 1;
-      // the next item's flag: its last readers are past the barrier of the item before this one
-      if (st == 0) sm.poison[item3] = 0;
       bar_sync(5, 256);
       l += sm.lx[half ^ 1][row];
       const bool poison = sm.poison[mine3] != 0;
       wait_warp(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, a.status);
       tc_fence_after();
       if (warp_live) {
-        const size_t orow = (size_t)(it.t0 + tok) * a.Hq + it.kvh * G + (row - tok * G);
-        const size_t prow_out = (size_t)max(it.part, 0) * kRows + row;
+        const size_t orow = (size_t)(it.t0 + tok) * a.Hq + it.kvh * G + (trow - tok * G);
+        const size_t prow_out = (size_t)max(it.part, 0) * (2 * kRows) + trow;
         const float inv = l == 0.f ? 0.f : vmul / l;
 #pragma unroll 1
         for (int c = 0; c < OC; c += 32) {
@@ -569,69 +658,90 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           else if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
         }
       }
-      if (it.n_parts > 0 && st == 0) ws.desc[blockIdx.x] = ChunkDesc{it.n_parts, it.t0, it.ntok, it.kvh};
+      if (it.n_parts > 0 && st == 0 && rank == 0) ws.desc[worker] = ChunkDesc{it.n_parts, it.t0, it.ntok, it.kvh};
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.o_free);
+      if (lane == 0) arrive_at(o_free0);
       it = nx;
       have = have_next;
     }
-  } else if (FP8 && warp >= 12) {
+  } else if constexpr (FP8) {
     // ---------------- codes to FP16 ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegConv));
     const int ct = threadIdx.x - 384;                  // 0 .. 127
     uint32_t r = 0, rphase = 0;
     while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
-      const int total = 2 * DB * (it.blk_hi - it.blk_lo);
-      for (int i = 0; ok && i < total; ++i) {
+      const int n = it.blk_hi - it.blk_lo;
+      for (int i = 0; ok && i < 2 * n; ++i) {
+        const bool key = i == 0 || (i != 2 * n - 1 && (i & 1));   // K0, K1, V0, K2, V1, ..., V of the last tile
         ok = wait_warp(&sm.raw_full[r], rphase, abort_flag, a.status) &&
              wait_warp(&sm.empty[s], phase ^ 1, abort_flag, a.status);
         if (!ok) break;
+        const unsigned char* src = sm.raw[C::kRaws ? r : 0];
+        unsigned char* dst = sm.stage[s];
+        constexpr int N = C::kRaw / 16 / 128;          // 16-byte vectors of a thread
+        constexpr int NB = N < 4 ? N : 4;              // loaded ahead
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int idx = k * 128 + ct, tr = idx >> 2, c = idx & 3;
-          const uint4 x = *reinterpret_cast<const uint4*>(sm.raw[C::kRaw ? r : 0] + idx * 16);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          uint32_t h[8];
+        for (int k0 = 0; k0 < N; k0 += NB) {
+          uint4 x[NB];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] & 0xffffu), __NV_E4M3);
-            const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] >> 16), __NV_E4M3);
-            h[2 * e] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
-            h[2 * e + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
+          for (int k = 0; k < NB; ++k) x[k] = *reinterpret_cast<const uint4*>(src + ((k0 + k) * 128 + ct) * 16);
+#pragma unroll
+          for (int k = 0; k < NB; ++k) {
+            const int idx = (k0 + k) * 128 + ct;
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] & 0xffffu), __NV_E4M3);
+              const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] >> 16), __NV_E4M3);
+              h[2 * e] = (uint32_t)lo.x | ((uint32_t)lo.y << 16);
+              h[2 * e + 1] = (uint32_t)hi.x | ((uint32_t)hi.y << 16);
+            }
+            // rows of 64 codes (32 in a value half at D = 64) become rows of 128 (64) bytes, swizzled
+            uint32_t o0, o1;
+            if (D >= 128 || key) {
+              const int tr = idx >> 2, c = 2 * (idx & 3);
+              o0 = tr * 128 + ((c ^ (tr & 7)) << 4), o1 = tr * 128 + (((c + 1) ^ (tr & 7)) << 4);
+            } else {
+              const int tr = idx >> 1, c = 2 * (idx & 1);
+              o0 = tr * 64 + ((c ^ ((tr >> 1) & 3)) << 4), o1 = tr * 64 + (((c + 1) ^ ((tr >> 1) & 3)) << 4);
+            }
+            *reinterpret_cast<uint4*>(dst + o0) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + o1) = make_uint4(h[4], h[5], h[6], h[7]);
           }
-          unsigned char* dst = sm.slot[s] + tr * 128;
-          *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (tr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (tr & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         async_fence();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sm.full[s]);
+          arrive_at(map_cta(saddr(&sm.full[s]), 0));
           mbar_arrive(&sm.raw_empty[r]);
         }
-        if (++s == C::kSlots) s = 0, phase ^= 1;
-        if (++r == (uint32_t)C::kRaw) r = 0, rphase ^= 1;
+        if (++s == C::kStages) s = 0, phase ^= 1;
+        if (++r == (uint32_t)C::kRaws) r = 0, rphase ^= 1;
       }
     }
   }
 
   // ---- teardown
   tc_fence_before();
+  __syncwarp();
   __syncthreads();
-  if (*abort_flag) {   // nothing may still be in flight when the CTA leaves
-    if (threadIdx.x == 0) {
-      // slots below s were last armed in this round, the others in the one before
-      for (int i = 0; i < (FP8 ? C::kRaw : C::kSlots); ++i)
-        mbar_drain(FP8 ? &sm.raw_full[i] : &sm.full[i], i < (int)s ? phase : phase ^ 1);
+  if (*abort_flag) {   // nothing may still be in flight when a CTA of the pair leaves
+    if (threadIdx.x == 0 && (FP8 || rank == 0)) {
+      // stages below s were last armed in this round, the others in the one before
+      for (int i = 0; i < (FP8 ? C::kRaws : C::kStages); ++i)
+        mbar_drain(FP8 ? &sm.raw_full[FP8 ? i : 0] : &sm.full[FP8 ? 0 : i], i < (int)s ? phase : phase ^ 1);
     } else if (threadIdx.x == 32 && issued) {
-      umma::commit(&sm.drain);
+      commit_pair(&sm.drain);
       mbar_drain(&sm.drain, 0);
     }
     __syncthreads();
   }
+  cluster_sync();      // the other CTA's operands, TMEM and barriers are used up to here
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
   }
 }
 
@@ -639,14 +749,14 @@ template <int D, bool FP8>
 cudaError_t launch(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk, float vmul, cudaStream_t s) {
   CUtensorMap mk, mv;
   if (!chunk_cache_map(&mk, a.k_pages, a, FP8, 64, kPageTokens, FP8 ? 0 : 128) ||
-      !chunk_cache_map(&mv, a.v_pages, a, FP8, 64, kPageTokens, FP8 ? 0 : 128))
+      !chunk_cache_map(&mv, a.v_pages, a, FP8, D >= 128 ? 64 : 32, kPageTokens, FP8 ? 0 : Cfg<D, FP8>::VR))
     return cudaErrorInvalidValue;
   auto kern = chunk_tc_kernel<D, FP8>;
   constexpr size_t smem = sizeof(TcSmem<D, FP8>) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(grid), dim3(Cfg<D, FP8>::kThreads), smem, s, 1, a, ws, qk, vmul, mk, mv);
+  return launch_k(kern, dim3(grid & ~1), dim3(Cfg<D, FP8>::kThreads), smem, s, 2, a, ws, qk, vmul, mk, mv);
 }
 template <int D>
 cudaError_t launch_kv(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk, float vmul, cudaStream_t s) {
@@ -658,7 +768,7 @@ cudaError_t launch_kv(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk,
 bool chunk_tc_supported(const ChunkArgs& a) {
   return a.q_dt == QSA_BF16 && (a.kv_dt == QSA_BF16 || a.kv_dt == QSA_FP8_E4M3);
 }
-int chunk_tc_rows() { return kRows; }
+int chunk_tc_rows() { return 2 * kRows; }
 cudaError_t launch_chunk_attn_tc(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk, float vmul, cudaStream_t s) {
   switch (a.D) {
     case 64: return launch_kv<64>(a, ws, grid, qk, vmul, s);

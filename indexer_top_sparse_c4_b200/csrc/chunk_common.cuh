@@ -8,7 +8,7 @@ namespace qsa {
 
 constexpr int kChunkMaxReq = 1024;   // requests per chunk-attention call
 constexpr int kChunkMaxTiles = 1024; // query tiles per KV head of a call whose tiles are split over CTAs
-constexpr int kChunkMaxCtas = 148;   // CTAs that leave partials (one per SM of a B200)
+constexpr int kChunkMaxCtas = 148;   // CTAs that leave partials (one per SM of a B200; half as many pairs)
 
 // A request as the device arrays give it.  `kv` is capped to the tokens a row
 // of the page table can address.
@@ -100,7 +100,8 @@ __device__ __forceinline__ int chunk_find(const int* v, int n, int x) {
 
 // Called by every thread of the CTA; the table is ready on return.  share: tiles
 // are split over CTAs however many there are (as far as the table holds them).
-__device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched& s, int TPT, int KT, bool share) {
+__device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched& s, int TPT, int KT, int workers,
+                                                  bool share) {
   int carry = 0;
   for (int base = 0; base < a.B; base += blockDim.x) {
     const int b = base + threadIdx.x;
@@ -112,7 +113,7 @@ __device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched
   if (threadIdx.x == 0) {
     s.first[a.B] = carry;
     s.nq = carry;
-    s.shared_tiles = carry <= kChunkMaxTiles && (share || (long long)carry * a.Hkv < 4ll * gridDim.x);
+    s.shared_tiles = carry <= kChunkMaxTiles && (share || (long long)carry * a.Hkv < 4ll * workers);
   }
   __syncthreads();
   if (s.shared_tiles) {
@@ -133,19 +134,21 @@ __device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched
   }
 }
 
-// A CTA's walk over its pieces; every warp role runs its own copy.
+// The walk of worker `me` of `all` (a CTA, or a pair of them) over its pieces;
+// every warp role runs its own copy.
 struct ChunkWalk {
   long long u, u1, total;  // shared tiles: linear blocks; otherwise u counts rounds
-  int ctas;                // CTAs that have work
+  int me, all, ctas;       // ctas: workers that have work
 
-  __device__ __forceinline__ void begin(const ChunkArgs& a, const ChunkSched& s) {
-    u = 0, u1 = 0, total = 0, ctas = gridDim.x;
+  __device__ __forceinline__ void begin(const ChunkArgs& a, const ChunkSched& s, int me_, int all_) {
+    me = me_, all = all_;
+    u = 0, u1 = 0, total = 0, ctas = all;
     if (s.shared_tiles) {
       total = (long long)s.blk[s.nq] * a.Hkv;
       if (total < ctas) ctas = (int)total;
-      if ((int)blockIdx.x < ctas) {
-        u = total * blockIdx.x / ctas;
-        u1 = total * (blockIdx.x + 1) / ctas;
+      if (me < ctas) {
+        u = total * me / ctas;
+        u1 = total * (me + 1) / ctas;
       }
     }
   }
@@ -163,17 +166,17 @@ struct ChunkWalk {
       it.blk_hi = left < it.nblk - it.blk_lo ? it.blk_lo + (int)left : it.nblk;
       it.part = -1, it.n_parts = 0;
       if (it.blk_lo > 0) {
-        it.part = 2 * blockIdx.x;
+        it.part = 2 * me;
       } else if (it.blk_hi < it.nblk) {
-        it.part = 2 * blockIdx.x + 1;
+        it.part = 2 * me + 1;
         const long long last = u + it.nblk - 1;                        // the tile's last linear block
         const int owner = (int)(((last + 1) * ctas - 1) / total);      // the CTA whose share holds it
-        it.n_parts = owner - (int)blockIdx.x + 1;
+        it.n_parts = owner - me + 1;
       }
       u += it.blk_hi - it.blk_lo;
     } else {
-      const long long idx = u * gridDim.x + ((u & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      if (u * gridDim.x >= (long long)s.nq * a.Hkv) return false;
+      const long long idx = u * all + ((u & 1) ? all - 1 - me : me);
+      if (u * all >= (long long)s.nq * a.Hkv) return false;
       ++u;
       if (idx >= (long long)s.nq * a.Hkv) return false;  // only in the last round
       it.kvh = (int)(idx / s.nq);
@@ -197,19 +200,21 @@ struct ChunkWalk {
 
 // Partials of the split tiles: unnormalised outputs [slot][row][D], then
 // (running maximum in base 2, sum) [slot][row], then the tiles' descriptors.
+// Two slots a worker; workers x rows of a tile is at most kChunkMaxCtas x 128.
+constexpr size_t kChunkWsRows = (size_t)2 * kChunkMaxCtas * 128;
 struct ChunkWs {
   float* o;
   float2* ml;
   ChunkDesc* desc;
 };
-__host__ __device__ __forceinline__ size_t chunk_ws_bytes(int rows, int D) {
-  return (size_t)2 * kChunkMaxCtas * rows * (D * sizeof(float) + sizeof(float2)) + kChunkMaxCtas * sizeof(ChunkDesc);
+__host__ __device__ __forceinline__ size_t chunk_ws_bytes(int D) {
+  return kChunkWsRows * (D * sizeof(float) + sizeof(float2)) + kChunkMaxCtas * sizeof(ChunkDesc);
 }
-__host__ __device__ __forceinline__ ChunkWs chunk_ws(void* ws, int rows, int D) {
+__host__ __device__ __forceinline__ ChunkWs chunk_ws(void* ws, int D) {
   ChunkWs w;
   w.o = reinterpret_cast<float*>(ws);
-  w.ml = reinterpret_cast<float2*>(w.o + (size_t)2 * kChunkMaxCtas * rows * D);
-  w.desc = reinterpret_cast<ChunkDesc*>(w.ml + (size_t)2 * kChunkMaxCtas * rows);
+  w.ml = reinterpret_cast<float2*>(w.o + kChunkWsRows * D);
+  w.desc = reinterpret_cast<ChunkDesc*>(w.ml + kChunkWsRows);
   return w;
 }
 
