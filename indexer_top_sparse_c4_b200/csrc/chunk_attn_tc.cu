@@ -119,14 +119,16 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       ::"r"(saddr(dst)), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// Addresses in the pair's CTAs, arrivals there.
+// Addresses in the pair's CTAs, arrivals there.  (The arrivals release at CTA
+// scope: what they publish lies in TMEM, ordered by tcgen05 fences, or in the
+// CTA's own shared memory; a release at cluster scope waits some 1,000 cycles.)
 __device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -494,11 +496,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       const int n_pages = (it.kv + kPageTokens - 1) / kPageTokens;
       const int32_t* pt = a.page_table + (size_t)it.b * a.pt_stride;
       float m = -INFINITY, l = 0.f;
-      int prow = page_row(a, pt, 2 * it.blk_lo + half, n_pages, false);   // this half's page of the tile
+      // this half's page of the tile, and the next one's (looked at a tile later)
+      auto page_of = [&](int lp) { return lp < n_pages ? __ldg(pt + lp) : -1; };
+      int page = page_of(2 * it.blk_lo + half);
       for (int j = 0; j < n; ++j) {
         const uint32_t buf = (g + j) & 1;
         const int key0 = (it.blk_lo + j) * kKeys + half * 64;
-        const int prow_next = j + 1 < n ? page_row(a, pt, 2 * (it.blk_lo + j + 1) + half, n_pages, false) : 0;
+        const int page_next = j + 1 < n ? page_of(2 * (it.blk_lo + j + 1) + half) : -1;
         wait_warp(&sm.s_full[buf], ((g + j) >> 1) & 1, abort_flag, a.status);
         tc_fence_after();
         if (warp_live) {
@@ -507,14 +511,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           tmem_ld32(ta, s);
           tmem_ld32(ta + 32, s + 32);
           tmem_wait_ld();
-          const int seen = prow < a.num_pages * kPageTokens ? lim - key0 : 0;
+          const int seen = page >= 0 && page < a.num_pages ? lim - key0 : 0;
           if (__any_sync(0xffffffffu, seen < 64)) {
 #pragma unroll
             for (int i = 0; i < 64; ++i) s[i] = i < seen ? s[i] : -INFINITY;
           }
-          float mx = s[0];
+          float mc[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 1; i < 64; ++i) mx = fmaxf(mx, s[i]);
+          for (int i = 4; i < 64; ++i) mc[i & 3] = fmaxf(mc[i & 3], s[i]);
+          float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
           sm.mx[buf][half][row] = mx;
           bar_sync(1 + quarter, 64);
           mx = fmaxf(mx, sm.mx[buf][half ^ 1][row]) * sc;
@@ -582,14 +587,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
               asm volatile("st.relaxed.cluster.shared::cluster.b32 [%0], %1;" ::"r"(map_cta(saddr(&sm.poison[item3]), cta)),
                            "r"(1)
                            : "memory");
-            asm volatile("fence.acq_rel.cluster;" ::: "memory");
           }
+          asm volatile("fence.acq_rel.cluster;" ::: "memory");
           async_fence();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_at(p_full0 + buf * 8);
-        prow = prow_next;
+        page = page_next;
       }
       // ---- the next item's Q goes in before this item's output goes out
       g += n;
