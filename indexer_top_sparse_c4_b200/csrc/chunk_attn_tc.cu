@@ -217,10 +217,21 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return r;
 }
 
-// A wait that gives up at once when the CTA is stopping.
+// One look at a phase.
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(saddr(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// A bounded wait that gives up at once when the CTA is stopping.  The first
+// look is the cheap one: a wait with a time limit costs some 200 cycles more.
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+  if (mbar_test(b, parity)) return true;
   if (*abort_flag) return false;
-  if (mbar_try_wait(b, parity)) return true;
   return mbar_wait(b, parity, abort_flag, status);
 }
 // The same by a whole warp, which is converged on return (the TMEM loads and
@@ -363,18 +374,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           }
         }
       }
-    } else if (warp == 1 && rank == 0) {
-      // ---------------- MMA issuer of the pair ----------------
+    } else if (warp == 1 && rank == 0 && lane == 0) {
+      // ---------------- MMA issuer of the pair (one thread) ----------------
       constexpr uint32_t kIdS = idesc(FP8, kKeys, false), kIdO = idesc(FP8, D, true);
       const uint64_t qd = umma::smem_desc(saddr(sm.q));
       const uint32_t ready0 = map_cta(saddr(&sm.v_ready), 0), ready1 = map_cta(saddr(&sm.v_ready), 1);
       uint32_t g = 0, item = 0;
       auto step = [&]() { if (++s == C::kStages) s = 0, phase ^= 1; };
       auto qk = [&](uint32_t buf) {
-        ok = ok && wait_warp(&sm.full[s], phase, abort_flag, a.status);
+        ok = ok && wait(&sm.full[s], phase, abort_flag, a.status);
         if (!ok) return;
-        if (lane == 0) {
-          tc_fence_after();
+        tc_fence_after();
+        {
           const uint64_t kd = umma::smem_desc(saddr(sm.stage[s]));
 #pragma unroll
           for (int db = 0; db < DB; ++db)
@@ -386,31 +397,29 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           commit_pair(&sm.empty[s]);
           issued = true;
         }
-        __syncwarp();
         step();
       };
       while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
         const int n = it.blk_hi - it.blk_lo;
         const int lim0 = min(it.p0 + 1, it.kv);
-        ok = wait_warp(&sm.q_full, item & 1, abort_flag, a.status);
+        ok = wait(&sm.q_full, item & 1, abort_flag, a.status);
         if (ok) qk(g & 1);
         for (int j = 0; ok && j < n; ++j) {
           const uint32_t buf = (g + j) & 1;
           if (j + 1 < n) qk(buf ^ 1);
           if (!ok) break;
-          if (j + 2 >= n && (j + 1 < n || n == 1) && lane == 0) commit_pair(&sm.q_empty);  // after the last Q K^T
-          __syncwarp();
+          if (j + 2 >= n && (j + 1 < n || n == 1)) commit_pair(&sm.q_empty);  // after the last Q K^T
           // the previous item's O has been read out before the first P V
-          if (j == 0) ok = wait_warp(&sm.o_free, (item & 1) ^ 1, abort_flag, a.status);
-          ok = ok && wait_warp(&sm.full[s], phase, abort_flag, a.status);
+          if (j == 0) ok = wait(&sm.o_free, (item & 1) ^ 1, abort_flag, a.status);
+          ok = ok && wait(&sm.full[s], phase, abort_flag, a.status);
           if (ok && (it.blk_lo + j + 1) * kKeys > lim0) {   // edge tile: the softmax warps clear V first
-            if (lane == 0) arrive_at(ready0), arrive_at(ready1);
-            __syncwarp();
+            arrive_at(ready0);
+            arrive_at(ready1);
           }
-          ok = ok && wait_warp(&sm.p_full[buf], ((g + j) >> 1) & 1, abort_flag, a.status);
+          ok = ok && wait(&sm.p_full[buf], ((g + j) >> 1) & 1, abort_flag, a.status);
           if (!ok) break;
-          if (lane == 0) {
-            tc_fence_after();
+          tc_fence_after();
+          {
             const uint64_t vd = v_desc<C::VR>(saddr(sm.stage[s]));
             const uint32_t p = tmem + kSCol + buf * kKeys;
             // 16 keys a step: 8 columns of P, 16 rows of V; keys 64.. of P start 64 columns on
@@ -421,7 +430,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             commit_pair(&sm.empty[s]);
             issued = true;
           }
-          __syncwarp();
           step();
         }
         g += n;
