@@ -234,6 +234,15 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile int*
   if (*abort_flag) return false;
   return mbar_wait(b, parity, abort_flag, status);
 }
+// One lane of a converged warp.  The compiler keeps the operands of MMAs issued
+// under it in uniform registers (16 MMAs take 153 cycles to issue); under a
+// comparison of the lane number it moves them there one by one (860 cycles,
+// more than the tensor cores need for a quarter of them).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 // The same by a whole warp, which is converged on return (the TMEM loads and
 // stores that follow need it).
 __device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
@@ -374,18 +383,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           }
         }
       }
-    } else if (warp == 1 && rank == 0 && lane == 0) {
-      // ---------------- MMA issuer of the pair (one thread) ----------------
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- MMA issuer of the pair ----------------
       constexpr uint32_t kIdS = idesc(FP8, kKeys, false), kIdO = idesc(FP8, D, true);
       const uint64_t qd = umma::smem_desc(saddr(sm.q));
       const uint32_t ready0 = map_cta(saddr(&sm.v_ready), 0), ready1 = map_cta(saddr(&sm.v_ready), 1);
       uint32_t g = 0, item = 0;
       auto step = [&]() { if (++s == C::kStages) s = 0, phase ^= 1; };
       auto qk = [&](uint32_t buf) {
-        ok = ok && wait(&sm.full[s], phase, abort_flag, a.status);
+        ok = ok && wait_warp(&sm.full[s], phase, abort_flag, a.status);
         if (!ok) return;
         tc_fence_after();
-        {
+        if (elect_one()) {
           const uint64_t kd = umma::smem_desc(saddr(sm.stage[s]));
 #pragma unroll
           for (int db = 0; db < DB; ++db)
@@ -395,31 +404,38 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                      kd + (db * (64 * 128) >> 4) + ks * 2, kIdS, (db | ks) != 0);
           commit_pair(&sm.s_full[buf]);
           commit_pair(&sm.empty[s]);
-          issued = true;
         }
+        __syncwarp();
+        issued = true;
         step();
       };
       while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
         const int n = it.blk_hi - it.blk_lo;
         const int lim0 = min(it.p0 + 1, it.kv);
-        ok = wait(&sm.q_full, item & 1, abort_flag, a.status);
+        ok = wait_warp(&sm.q_full, item & 1, abort_flag, a.status);
         if (ok) qk(g & 1);
         for (int j = 0; ok && j < n; ++j) {
           const uint32_t buf = (g + j) & 1;
           if (j + 1 < n) qk(buf ^ 1);
           if (!ok) break;
-          if (j + 2 >= n && (j + 1 < n || n == 1)) commit_pair(&sm.q_empty);  // after the last Q K^T
-          // the previous item's O has been read out before the first P V
-          if (j == 0) ok = wait(&sm.o_free, (item & 1) ^ 1, abort_flag, a.status);
-          ok = ok && wait(&sm.full[s], phase, abort_flag, a.status);
-          if (ok && (it.blk_lo + j + 1) * kKeys > lim0) {   // edge tile: the softmax warps clear V first
-            arrive_at(ready0);
-            arrive_at(ready1);
+          if (j + 2 >= n && (j + 1 < n || n == 1)) {   // after the last Q K^T
+            if (elect_one()) commit_pair(&sm.q_empty);
+            __syncwarp();
           }
-          ok = ok && wait(&sm.p_full[buf], ((g + j) >> 1) & 1, abort_flag, a.status);
+          // the previous item's O has been read out before the first P V
+          if (j == 0) ok = wait_warp(&sm.o_free, (item & 1) ^ 1, abort_flag, a.status);
+          ok = ok && wait_warp(&sm.full[s], phase, abort_flag, a.status);
+          if (ok && (it.blk_lo + j + 1) * kKeys > lim0) {   // edge tile: the softmax warps clear V first
+            if (elect_one()) {
+              arrive_at(ready0);
+              arrive_at(ready1);
+            }
+            __syncwarp();
+          }
+          ok = ok && wait_warp(&sm.p_full[buf], ((g + j) >> 1) & 1, abort_flag, a.status);
           if (!ok) break;
           tc_fence_after();
-          {
+          if (elect_one()) {
             const uint64_t vd = v_desc<C::VR>(saddr(sm.stage[s]));
             const uint32_t p = tmem + kSCol + buf * kKeys;
             // 16 keys a step: 8 columns of P, 16 rows of V; keys 64.. of P start 64 columns on
@@ -428,8 +444,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
               mma_ts(tmem, p + (ks >> 2) * 64 + (ks & 3) * 8, vd + ks * (16 * C::VR >> 4), kIdO, j != 0 || ks != 0);
             commit_pair(&sm.pv_done[buf]);
             commit_pair(&sm.empty[s]);
-            issued = true;
           }
+          __syncwarp();
+          issued = true;
           step();
         }
         g += n;
@@ -745,8 +762,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       // stages below s were last armed in this round, the others in the one before
       for (int i = 0; i < (FP8 ? C::kRaws : C::kStages); ++i)
         mbar_drain(FP8 ? &sm.raw_full[FP8 ? i : 0] : &sm.full[FP8 ? 0 : i], i < (int)s ? phase : phase ^ 1);
-    } else if (threadIdx.x == 32 && issued) {
-      commit_pair(&sm.drain);
+    } else if (warp == 1 && issued) {
+      if (elect_one()) commit_pair(&sm.drain);
+      __syncwarp();
       mbar_drain(&sm.drain, 0);
     }
     __syncthreads();
