@@ -213,9 +213,10 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
   }
 }
 
-// Merges a tile that several CTAs share: blockIdx.x = the CTA that opened it,
-// blockIdx.y walks its rows.  A row's partials are spread over the 8 warps and
-// joined in shared memory in a fixed order.
+// Merges a tile that several workers share: blockIdx.x = the worker that opened
+// it, blockIdx.y walks its rows.  Up to 8 partials (chunks): a warp joins a row
+// by itself.  More (long decode rows): a row's partials are spread over the 8
+// warps and joined in shared memory.  The order of the sums is fixed.
 constexpr int kCombineThreads = 256;
 constexpr int kCombineY = 16;
 template <int D, typename OT>
@@ -231,6 +232,42 @@ __global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(ChunkArg
   if (dsc.n_parts == 0) return;
   const int G = a.Hq / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int first = 2 * blockIdx.x + 1;                 // then 2 (blockIdx.x + i), i = 1 .. n_parts - 1
+  if (dsc.n_parts <= W) {
+    for (int r = blockIdx.y * W + warp; r < dsc.ntok * G; r += kCombineY * W) {
+      // lane i: the maximum and sum of part i, and its weight
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < dsc.n_parts) ml = ws.ml[(size_t)(lane == 0 ? first : 2 * (blockIdx.x + lane)) * tile_rows + r];
+      float mx = ml.x;
+#pragma unroll
+      for (int d = 4; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      mx = __shfl_sync(0xffffffffu, mx, 0);
+      const float w = ml.x == mx ? 1.f : exp2f(ml.x - (mx == -INFINITY ? 0.f : mx));
+      float total = 0.f, o[VPT];
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) o[j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if (i >= dsc.n_parts) break;
+        float x[VPT];
+        VecLoad<float, VPT>::get(ws.o, ((size_t)(i == 0 ? first : 2 * (blockIdx.x + i)) * tile_rows + r) * D + lane * VPT, x);
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        total += __shfl_sync(0xffffffffu, ml.y, i) * wi;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) o[j] = fmaf(x[j], wi, o[j]);
+      }
+      const int tok = r / G;
+      const size_t row = (size_t)(dsc.t0 + tok) * a.Hq + dsc.kvh * G + (r - tok * G);
+      const float inv = total == 0.f ? 0.f : vmul / total;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        o[j] = total == 0.f ? 0.f : o[j] * inv;
+        if constexpr (sizeof(OT) == 4) reinterpret_cast<float*>(a.out)[row * D + lane * VPT + j] = o[j];
+        else reinterpret_cast<__nv_bfloat16*>(a.out)[row * D + lane * VPT + j] = __float2bfloat16_rn(o[j]);
+      }
+      if (a.lse && lane == 0) a.lse[row] = total == 0.f ? -INFINITY : mx * kLn2 + logf(total);
+    }
+    return;
+  }
   for (int r = blockIdx.y; r < dsc.ntok * G; r += kCombineY) {
     float m = -INFINITY, l = 0.f, o[VPT];
 #pragma unroll

@@ -77,7 +77,7 @@ struct Cfg {
   static constexpr int kQBytes = DB * kRows * 128;
   // Q and the rings take up to 208 KB
   static constexpr int kStages = FP8 ? (D == 256 ? 3 : 6) : (D == 256 ? 4 : 8);
-  static constexpr int kRaws = FP8 ? (D == 256 ? 3 : 6) : 0;
+  static constexpr int kRaws = FP8 ? (D == 256 ? 2 : 6) : 0;
   static constexpr int kThreads = FP8 ? 512 : 384;
   // registers after the split: loads and MMA, softmax, conversion (their sum is within the launch's 3 x 168 or 4 x 128)
   static constexpr int kRegLow = FP8 ? 64 : 72, kRegSoft = FP8 ? 184 : 216, kRegConv = 80;
@@ -99,8 +99,9 @@ struct TcSmem {
   uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, v_ready, drain;
   float mx[2][2][kRows];                 // [tile parity][half][row] maxima
   float lx[2][kRows];                    // [half][row] sums
-  float q_scale[kRows];                  // FP8: what undoes the row's power of two
-  int poison[3];                         // by item, modulo 3
+  float q_scale[2][kRows];               // FP8, by item parity: what undoes the row's power of two
+  alignas(16) unsigned char out[kSoftWarps][32 * 64];   // 64 bytes of a warp's 32 output rows
+  int poison[4];                         // by item, modulo 4
   uint32_t tmem_base;
   int abort_flag;
   ChunkSched sched;
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   const int G = a.Hq / a.Hkv, TPT = 2 * kRows / G;
   const uint32_t rank = cluster_rank();
   const int worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
+  const uint32_t g_inv = 65536u / G + 1;   // x / G = x * g_inv >> 16 for a tile's rows x < 256
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       mbar_init(&sm.raw_full[s], 1);
       mbar_init(&sm.raw_empty[s], 4);
     }
-    mbar_init(&sm.q_full, 2 * kSoftWarps);
+    mbar_init(&sm.q_full, 4);
     mbar_init(&sm.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 1);
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     mbar_init(&sm.v_ready, 1);
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
-    sm.poison[0] = sm.poison[1] = sm.poison[2] = 0;
+    sm.poison[0] = sm.poison[1] = sm.poison[2] = sm.poison[3] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -334,14 +336,21 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       constexpr int kRing = FP8 ? C::kRaws : C::kStages;
       constexpr uint32_t kBytes = FP8 ? C::kRaw : C::kStage;
       uint64_t* const empties = FP8 ? sm.raw_empty : sm.empty;
-      while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
-        const int n = it.blk_hi - it.blk_lo, lp0 = 2 * it.blk_lo;
-        const int n_pages = min((it.kv + kPageTokens - 1) / kPageTokens, lp0 + 2 * n);
-        const int32_t* pt = a.page_table + (size_t)it.b * a.pt_stride;
-        // rows of pages 32 w .. 32 w + 31 of this piece, and the next 32
-        int win = 0;
-        int cur = page_row(a, pt, lp0 + lane, n_pages, rank == 0);
-        int nxt = page_row(a, pt, lp0 + 32 + lane, n_pages, rank == 0);
+      // the cache rows of 32 pages of a piece, from its window w on
+      auto pages = [&](const ChunkItem& x, int w) {
+        const int lp0 = 2 * x.blk_lo;
+        const int n_pages = min((x.kv + kPageTokens - 1) / kPageTokens, 2 * x.blk_hi);
+        return page_row(a, a.page_table + (size_t)x.b * a.pt_stride, lp0 + 32 * w + lane, n_pages, rank == 0);
+      };
+      ChunkItem nx;
+      bool have = walk.next(a, sm.sched, TPT, kKeys, it);
+      int first = have ? pages(it, 0) : 0;
+      for (; ok && have && !*abort_flag; it = nx) {
+        const int n = it.blk_hi - it.blk_lo;
+        int win = 0, cur = first, nxt = n > 16 ? pages(it, 1) : 0;
+        // the next piece is found, and its pages, while this one streams
+        have = walk.next(a, sm.sched, TPT, kKeys, nx);
+        first = have ? pages(nx, 0) : 0;
         auto load = [&](bool key, int j) {
           const int x = 2 * j, from = (x >> 5) == win ? cur : nxt;
           const int y0 = __shfl_sync(0xffffffffu, from, x & 31), y1 = __shfl_sync(0xffffffffu, from, (x + 1) & 31);
@@ -379,7 +388,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           if (((2 * j + 2) >> 5) != win) {   // the next V tile lies in the next window
             ++win;
             cur = nxt;
-            nxt = page_row(a, pt, lp0 + 32 * (win + 1) + lane, n_pages, rank == 0);
+            nxt = pages(it, win + 1);
           }
         }
       }
@@ -409,11 +418,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         issued = true;
         step();
       };
-      while (ok && !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it)) {
+      ChunkItem nx;
+      bool have = walk.next(a, sm.sched, TPT, kKeys, it);
+      for (; ok && have && !*abort_flag; it = nx) {
         const int n = it.blk_hi - it.blk_lo;
         const int lim0 = min(it.p0 + 1, it.kv);
         ok = wait_warp(&sm.q_full, item & 1, abort_flag, a.status);
         if (ok) qk(g & 1);
+        have = walk.next(a, sm.sched, TPT, kKeys, nx);
         for (int j = 0; ok && j < n; ++j) {
           const uint32_t buf = (g + j) & 1;
           if (j + 1 < n) qk(buf ^ 1);
@@ -452,6 +464,55 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         g += n;
         ++item;
       }
+    } else if (warp >= 2) {
+      // ---------------- Q of the next item: this CTA's rows into shared memory ----------------
+      // (128-byte swizzle, K-major; rows past the item's tokens keep what they
+      // held, which reaches nothing but those rows)
+      constexpr int CH = D / 8, RP = 64 / CH;          // 16-byte chunks of a row, rows of a pass of 64 threads
+      constexpr int NB = 8;                            // loads in flight of a thread
+      const int lt = threadIdx.x - 64, c = lt % CH;
+      const uint32_t q_full0 = map_cta(saddr(&sm.q_full), 0);
+      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
+      unsigned char* const dst = sm.q + (c >> 3) * (kRows * 128);
+      for (uint32_t item = 0; !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it); ++item) {
+        const int rows = min(it.ntok * G - (int)rank * kRows, kRows);   // this CTA's
+        const __nv_bfloat16* qi = q + ((size_t)it.t0 * a.Hq + it.kvh * G) * D + c * 8;
+        if (!wait_warp(&sm.q_empty, (item & 1) ^ 1, abort_flag, a.status)) break;
+        for (int r0 = 0; r0 < rows; r0 += NB * RP) {
+          uint4 v[NB];
+#pragma unroll
+          for (int k = 0; k < NB; ++k) {
+            const int r = r0 + k * RP + lt / CH, tr = (int)rank * kRows + r;
+            const int tok = (int)((uint32_t)tr * g_inv >> 16);
+            v[k] = r < rows ? *reinterpret_cast<const uint4*>(qi + ((size_t)tok * a.Hq + (tr - tok * G)) * D)
+                            : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < NB; ++k) {
+            const int r = r0 + k * RP + lt / CH;
+            if constexpr (FP8) {
+              uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+              uint32_t top = 0;                        // the row's largest exponent field
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = max(top, max((w[e] >> 7) & 0xffu, (w[e] >> 23) & 0xffu));
+#pragma unroll
+              for (int x = 1; x < CH; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+              const uint32_t E = min(max(top, 11u), 254u);
+              const float up = __uint_as_float((264u - E) << 23);    // 2^(137 - E): the largest lands in 2^10 .. 2^11
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack16<true>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
+              v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+              if (c == 0 && r < rows) sm.q_scale[item & 1][r] = __uint_as_float((E - 10u) << 23);  // 2^(E - 137)
+            }
+            if (r < rows) *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[k];
+          }
+        }
+        async_fence();
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive_at(q_full0);
+      }
     }
   } else if (warp < 4 + kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
@@ -461,59 +522,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
     const int row = 32 * quarter + lane;
     const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
     constexpr int OC = D / 2;                          // columns of O per thread
-    const uint32_t q_full0 = map_cta(saddr(&sm.q_full), 0), o_free0 = map_cta(saddr(&sm.o_free), 0);
+    const uint32_t o_free0 = map_cta(saddr(&sm.o_free), 0);
     const uint32_t p_full0 = map_cta(saddr(&sm.p_full[0]), 0);
-    uint32_t g = 0, item = 0, item3 = 0;               // tiles, items so far
+    uint32_t g = 0, item = 0;                          // tiles, items so far
     uint32_t pos = 0, edges = 0;                       // ring stage of the item's first K; edge tiles so far
 
-    // Q of the next item into shared memory (128-byte swizzle, K-major); rows
-    // past its tokens are zero
-    auto load_q = [&](const ChunkItem& x) -> float {
-      wait_warp(&sm.q_empty, (item & 1) ^ 1, abort_flag, a.status);
-      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
-      constexpr int CH = D / 8;                        // 16-byte chunks per row
-      const int rows = x.ntok * G;
-#pragma unroll 4
-      for (int i = st; i < kRows * CH; i += 256) {
-        const int r = i / CH, c = i % CH, tr = (int)rank * kRows + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (tr < rows)
-          v = *reinterpret_cast<const uint4*>(q + ((size_t)(x.t0 + tr / G) * a.Hq + x.kvh * G + tr % G) * D + c * 8);
-        if constexpr (FP8) {
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t top = 0;                            // the row's largest exponent field
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top = max(top, max((w[k] >> 7) & 0xffu, (w[k] >> 23) & 0xffu));
-#pragma unroll
-          for (int d = 1; d < CH; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const uint32_t E = min(max(top, 11u), 254u);
-          const float up = __uint_as_float((264u - E) << 23);    // 2^(137 - E): the largest lands in 2^10 .. 2^11
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = pack16<true>(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
-          v = make_uint4(w[0], w[1], w[2], w[3]);
-          if (c == 0) sm.q_scale[r] = __uint_as_float((E - 10u) << 23);  // 2^(E - 137)
-        }
-        *reinterpret_cast<uint4*>(sm.q + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-      }
-      async_fence();
-      __syncwarp();
-      if (lane == 0) arrive_at(q_full0);
-      float sc = qk_scale_log2;
-      if constexpr (FP8) {
-        bar_sync(5, 256);
-        sc = fmaxf(sc * sm.q_scale[row], 1.2e-38f);   // 0 x -inf below would be NaN; the logits are 0 either way
-      }
-      return sc;
-    };
-
+    const int trow = (int)rank * kRows + row, tok = (int)((uint32_t)trow * g_inv >> 16);
     ChunkItem nx;
     bool have = walk.next(a, sm.sched, TPT, kKeys, it);
-    float sc_next = have ? load_q(it) : 0.f;
     while (have) {
-      const float sc = sc_next;
+      const bool have_next = walk.next(a, sm.sched, TPT, kKeys, nx);   // before the first wait
       const int n = it.blk_hi - it.blk_lo, rows = it.ntok * G;
-      const int trow = (int)rank * kRows + row, tok = trow / G;
+      float sc = qk_scale_log2;
       const bool live = trow < rows;                   // this thread's row is a query
       const bool warp_live = (int)rank * kRows + 32 * quarter < rows;
       const int lim = live ? min(it.p0 + tok + 1, it.kv) : 0;   // keys the row sees
@@ -530,6 +550,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         const int page_next = j + 1 < n ? page_of(2 * (it.blk_lo + j + 1) + half) : -1;
         wait_warp(&sm.s_full[buf], ((g + j) >> 1) & 1, abort_flag, a.status);
         tc_fence_after();
+        // never 0: 0 x -inf would be NaN where the logit is 0
+        if (FP8 && j == 0 && live) sc = fmaxf(qk_scale_log2 * sm.q_scale[item & 1][row], 1.2e-38f);
         if (warp_live) {
           float s[64];
           const uint32_t ta = tlane + kSCol + buf * kKeys + half * 64;
@@ -609,7 +631,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           if (odd) {   // both CTAs' rows may see it
 #pragma unroll
             for (uint32_t cta = 0; cta < 2; ++cta)
-              asm volatile("st.relaxed.cluster.shared::cluster.b32 [%0], %1;" ::"r"(map_cta(saddr(&sm.poison[item3]), cta)),
+              asm volatile("st.relaxed.cluster.shared::cluster.b32 [%0], %1;" ::"r"(map_cta(saddr(&sm.poison[item & 3]), cta)),
                            "r"(1)
                            : "memory");
           }
@@ -621,40 +643,60 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         if (lane == 0) arrive_at(p_full0 + buf * 8);
         page = page_next;
       }
-      // ---- the next item's Q goes in before this item's output goes out
+      // ---- output
       g += n;
       pos = (pos + 2 * n) % C::kStages;
-      ++item;
-      const uint32_t mine3 = item3;
-      item3 = item3 == 2 ? 0 : item3 + 1;
-      // The next item's flag: its last readers are past the barrier of the item
-      // before this one, its writers behind the arrivals for the next Q.
-      if (st == 0) sm.poison[item3] = 0;
-      const bool have_next = walk.next(a, sm.sched, TPT, kKeys, nx);
-      if (have_next) sc_next = load_q(nx);
+      // The flag of the item after next: its last readers are past the barrier of
+      // the item before this one, its writers behind the P of the next one.
+      if (st == 0) sm.poison[(item + 2) & 3] = 0;
       sm.lx[half][row] = l;
       bar_sync(5, 256);
       l += sm.lx[half ^ 1][row];
-      const bool poison = sm.poison[mine3] != 0;
+      const bool poison = sm.poison[item & 3] != 0;
       wait_warp(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, a.status);
       tc_fence_after();
       if (warp_live) {
         const size_t orow = (size_t)(it.t0 + tok) * a.Hq + it.kvh * G + (trow - tok * G);
         const size_t prow_out = (size_t)max(it.part, 0) * (2 * kRows) + trow;
         const float inv = l == 0.f ? 0.f : vmul / l;
+        // 64 bytes of each of the warp's rows go through shared memory, so that
+        // four lanes store a row's: 8 rows x 64 bytes an instruction, not 32 x 16
+        unsigned char* const so = sm.out[warp - 4];
+        size_t drow[4];                                // rows 8 k + lane / 4 of the warp
+        bool dlive[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tr = (int)rank * kRows + 32 * quarter + 8 * k + (lane >> 2);
+          const int tk = (int)((uint32_t)tr * g_inv >> 16);
+          dlive[k] = tr < rows;
+          drow[k] = it.part < 0 ? (size_t)(it.t0 + tk) * a.Hq + it.kvh * G + (tr - tk * G)
+                                : (size_t)it.part * (2 * kRows) + tr;
+        }
+        auto put = [&](int ch, uint4 v) {              // this thread's row, 16-byte chunk ch
+          *reinterpret_cast<uint4*>(so + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) = v;
+        };
+        auto flush = [&](void* base, int row_bytes, int byte0) {
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = 8 * k + (lane >> 2), ch = lane & 3;
+            const uint4 v = *reinterpret_cast<const uint4*>(so + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4));
+            if (dlive[k])
+              *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(base) + drow[k] * row_bytes + byte0 + ch * 16) = v;
+          }
+          __syncwarp();
+        };
 #pragma unroll 1
         for (int c = 0; c < OC; c += 32) {
           float o[32];
-          __syncwarp();
           tmem_ld32(tlane + half * OC + c, o);
           tmem_wait_ld();
-          if (!live) continue;
           const int col = half * OC + c;
           if (l == 0.f) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0.f;
           }
-          if (poison) {  // non-finite values of the edge tiles that this row sees
+          if (poison && live) {  // non-finite values of the edge tiles that this row sees
             const int from = max(it.blk_lo, max(lim0, 0) / kKeys) * kKeys, to = min(lim, it.blk_hi * kKeys);
             for (int t = from; t < to; ++t) {
               const int pr = page_row(a, pt, t / kPageTokens, n_pages, false);
@@ -670,17 +712,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
             }
           }
           if (it.part < 0) {
-            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + orow * D + col);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack16<false>(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                  pack16<false>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                  pack16<false>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                  pack16<false>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+              put(i, make_uint4(pack16<false>(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                pack16<false>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                pack16<false>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                pack16<false>(o[8 * i + 6] * inv, o[8 * i + 7] * inv)));
+            flush(a.out, D * 2, col * 2);
           } else {
-            float4* dst = reinterpret_cast<float4*>(ws.o + prow_out * D + col);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                put(i, make_uint4(__float_as_uint(o[16 * h + 4 * i]), __float_as_uint(o[16 * h + 4 * i + 1]),
+                                  __float_as_uint(o[16 * h + 4 * i + 2]), __float_as_uint(o[16 * h + 4 * i + 3])));
+              flush(ws.o, D * 4, (col + 16 * h) * 4);
+            }
           }
         }
         if (live && half == 0) {
@@ -692,6 +739,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(o_free0);
+      ++item;
       it = nx;
       have = have_next;
     }
