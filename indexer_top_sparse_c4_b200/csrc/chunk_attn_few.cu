@@ -43,6 +43,7 @@ using namespace mbar;
 constexpr float kGrow = 8.f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kStep = 16;  // keys of a step
+constexpr int kLead = 4;   // what a tile costs beside its blocks of 64 keys, in blocks
 
 template <int D, bool FP8, int NT>
 struct FewCfg {
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) ws.desc[blockIdx.x].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, KT, gridDim.x, true);
+  chunk_sched_build(a, sm.sched, TPT, KT, gridDim.x, true, kLead);
 
   // Keys this tile's last row sees, and the steps of a piece that hold any.
   auto steps_of = [&](const ChunkItem& x) {

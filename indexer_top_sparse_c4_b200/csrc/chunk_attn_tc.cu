@@ -64,6 +64,7 @@ constexpr int kKeys = 128;               // keys of a tile: two pages
 constexpr uint32_t kSCol = 256;          // first TMEM column of the S tiles
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSoftWarps = 8;
+constexpr int kLead = 4;                 // what a tile costs beside its blocks, in blocks
 constexpr float kGrow = 8.f;             // log2 of how far P may grow before O is rescaled
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0 && rank == 0) ws.desc[worker].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, kKeys, workers, false);
+  chunk_sched_build(a, sm.sched, TPT, kKeys, workers, false, kLead);
   ChunkWalk walk;
   walk.begin(a, sm.sched, worker, workers);
   ChunkItem it;
@@ -469,28 +470,35 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       // (128-byte swizzle, K-major; rows past the item's tokens keep what they
       // held, which reaches nothing but those rows)
       constexpr int CH = D / 8, RP = 64 / CH;          // 16-byte chunks of a row, rows of a pass of 64 threads
-      constexpr int NB = 8;                            // loads in flight of a thread
       const int lt = threadIdx.x - 64, c = lt % CH;
       const uint32_t q_full0 = map_cta(saddr(&sm.q_full), 0);
       const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q);
       unsigned char* const dst = sm.q + (c >> 3) * (kRows * 128);
+      auto at = [&](int r) { return reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
       for (uint32_t item = 0; !*abort_flag && walk.next(a, sm.sched, TPT, kKeys, it); ++item) {
         const int rows = min(it.ntok * G - (int)rank * kRows, kRows);   // this CTA's
         const __nv_bfloat16* qi = q + ((size_t)it.t0 * a.Hq + it.kvh * G) * D + c * 8;
         if (!wait_warp(&sm.q_empty, (item & 1) ^ 1, abort_flag, a.status)) break;
-        for (int r0 = 0; r0 < rows; r0 += NB * RP) {
-          uint4 v[NB];
+        // all of it in flight at once
+#pragma unroll 4
+        for (int r = lt / CH; r < rows; r += RP) {
+          const int tr = (int)rank * kRows + r, tok = (int)((uint32_t)tr * g_inv >> 16);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr(at(r))),
+                       "l"(qi + ((size_t)tok * a.Hq + (tr - tok * G)) * D)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (FP8) {                           // to FP16 in place, each thread what it brought
+          for (int r0 = 0; r0 < rows; r0 += 4 * RP) {
+            uint4 v[4];
 #pragma unroll
-          for (int k = 0; k < NB; ++k) {
-            const int r = r0 + k * RP + lt / CH, tr = (int)rank * kRows + r;
-            const int tok = (int)((uint32_t)tr * g_inv >> 16);
-            v[k] = r < rows ? *reinterpret_cast<const uint4*>(qi + ((size_t)tok * a.Hq + (tr - tok * G)) * D)
-                            : make_uint4(0, 0, 0, 0);
-          }
+            for (int k = 0; k < 4; ++k) {
+              const int r = r0 + k * RP + lt / CH;
+              v[k] = r < rows ? *at(r) : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-          for (int k = 0; k < NB; ++k) {
-            const int r = r0 + k * RP + lt / CH;
-            if constexpr (FP8) {
+            for (int k = 0; k < 4; ++k) {
+              const int r = r0 + k * RP + lt / CH;
               uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
               uint32_t top = 0;                        // the row's largest exponent field
 #pragma unroll
@@ -502,10 +510,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 w[e] = pack16<true>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
-              v[k] = make_uint4(w[0], w[1], w[2], w[3]);
-              if (c == 0 && r < rows) sm.q_scale[item & 1][r] = __uint_as_float((E - 10u) << 23);  // 2^(E - 137)
+              if (r < rows) {
+                *at(r) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (c == 0) sm.q_scale[item & 1][r] = __uint_as_float((E - 10u) << 23);  // 2^(E - 137)
+              }
             }
-            if (r < rows) *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[k];
           }
         }
         async_fence();

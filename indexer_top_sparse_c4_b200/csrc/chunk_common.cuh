@@ -44,17 +44,19 @@ struct ChunkDesc {
 
 // The cut of a call's work.  Query tiles hold TPT tokens of one request (all
 // query heads of one KV head); their keys fall into blocks of KT.  With few
-// tiles the linear (KV head, tile, block) space is divided evenly over the
-// CTAs, whatever the requests' lengths, and tiles that several CTAs share
-// are merged by the combine kernel.  With many tiles (four per CTA, or more
+// tiles the linear (KV head, tile, unit) space is divided evenly over the
+// workers, whatever the requests' lengths, and tiles that several share are
+// merged by the combine kernel.  A tile's units are its key blocks behind a
+// lead: what its start and end cost, in blocks, so that a worker with many
+// short tiles does not finish last.  With many tiles (four per CTA, or more
 // than the table holds) every tile is one CTA's; neighbouring CTAs then walk
 // the same keys at about the same time and share them in L2, and rounds run
 // in alternating order so that the causal tiles' growing lengths even out.
 struct ChunkSched {
   int first[kChunkMaxReq + 1];    // query tiles before each request
-  int blk[kChunkMaxTiles + 1];    // shared tiles: key blocks before each query tile
+  int blk[kChunkMaxTiles + 1];    // shared tiles: units before each query tile (its lead and its key blocks)
   int warp_sum[32];
-  int nq, shared_tiles;
+  int nq, shared_tiles, lead;
 };
 
 // Exclusive prefix sum of v over the CTA's threads plus `carry`; returns this
@@ -99,9 +101,9 @@ __device__ __forceinline__ int chunk_find(const int* v, int n, int x) {
 }
 
 // Called by every thread of the CTA; the table is ready on return.  share: tiles
-// are split over CTAs however many there are (as far as the table holds them).
+// are split over workers however many there are (as far as the table holds them).
 __device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched& s, int TPT, int KT, int workers,
-                                                  bool share) {
+                                                  bool share, int lead) {
   int carry = 0;
   for (int base = 0; base < a.B; base += blockDim.x) {
     const int b = base + threadIdx.x;
@@ -113,6 +115,7 @@ __device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched
   if (threadIdx.x == 0) {
     s.first[a.B] = carry;
     s.nq = carry;
+    s.lead = lead;
     s.shared_tiles = carry <= kChunkMaxTiles && (share || (long long)carry * a.Hkv < 4ll * workers);
   }
   __syncthreads();
@@ -124,7 +127,7 @@ __device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched
       int n = 0;
       if (q < nq) {
         const int b = chunk_find(s.first, a.B, q);
-        n = chunk_tile_blocks(chunk_req(a, b, false), q - s.first[b], TPT, KT);
+        n = lead + chunk_tile_blocks(chunk_req(a, b, false), q - s.first[b], TPT, KT);
       }
       const int before = chunk_scan(n, s.warp_sum, carry);
       if (q < nq) s.blk[q] = before;
@@ -135,45 +138,60 @@ __device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched
 }
 
 // The walk of worker `me` of `all` (a CTA, or a pair of them) over its pieces;
-// every warp role runs its own copy.
+// every warp role runs its own copy.  A step costs a few shared-memory reads:
+// the next tile follows from the last one, only the first is searched for.
 struct ChunkWalk {
-  long long u, u1, total;  // shared tiles: linear blocks; otherwise u counts rounds
+  long long u, u1, total;  // shared tiles: units left to walk; otherwise u counts rounds
   int me, all, ctas;       // ctas: workers that have work
+  int kvh, q, x, b;        // shared tiles: KV head, tile, unit within the tile, request
 
   __device__ __forceinline__ void begin(const ChunkArgs& a, const ChunkSched& s, int me_, int all_) {
     me = me_, all = all_;
     u = 0, u1 = 0, total = 0, ctas = all;
+    kvh = q = x = b = 0;
     if (s.shared_tiles) {
-      total = (long long)s.blk[s.nq] * a.Hkv;
+      const int wq = s.blk[s.nq];
+      total = (long long)wq * a.Hkv;
       if (total < ctas) ctas = (int)total;
       if (me < ctas) {
         u = total * me / ctas;
         u1 = total * (me + 1) / ctas;
+        kvh = (int)(u / wq);
+        const int y = (int)(u - (long long)kvh * wq);
+        q = chunk_find(s.blk, s.nq, y);
+        x = y - s.blk[q];
+        b = chunk_find(s.first, a.B, q);
       }
     }
   }
   __device__ __forceinline__ bool next(const ChunkArgs& a, const ChunkSched& s, int TPT, int KT, ChunkItem& it) {
-    int q;
+    int tile;
     if (s.shared_tiles) {
-      if (u >= u1) return false;
-      const int wq = s.blk[s.nq];
-      it.kvh = (int)(u / wq);
-      const int x = (int)(u - (long long)it.kvh * wq);
-      q = chunk_find(s.blk, s.nq, x);
-      it.blk_lo = x - s.blk[q];
-      it.nblk = s.blk[q + 1] - s.blk[q];
-      const long long left = u1 - u;
-      it.blk_hi = left < it.nblk - it.blk_lo ? it.blk_lo + (int)left : it.nblk;
-      it.part = -1, it.n_parts = 0;
-      if (it.blk_lo > 0) {
-        it.part = 2 * me;
-      } else if (it.blk_hi < it.nblk) {
-        it.part = 2 * me + 1;
-        const long long last = u + it.nblk - 1;                        // the tile's last linear block
-        const int owner = (int)(((last + 1) * ctas - 1) / total);      // the CTA whose share holds it
-        it.n_parts = owner - me + 1;
+      for (;;) {   // a piece that would hold no block (a tile's lead alone) is passed over
+        if (u >= u1) return false;
+        while (s.first[b + 1] <= q) ++b;
+        const int units = s.blk[q + 1] - s.blk[q], nblk = units - s.lead;
+        const int take = u1 - u < units - x ? (int)(u1 - u) : units - x;
+        it.kvh = kvh, it.b = b, it.nblk = nblk;
+        it.blk_lo = max(0, x - s.lead), it.blk_hi = x + take - s.lead;
+        it.part = -1, it.n_parts = 0;
+        tile = q - s.first[b];
+        if (it.blk_lo > 0) {
+          it.part = 2 * me;
+        } else if (it.blk_hi < nblk) {
+          it.part = 2 * me + 1;
+          const long long last = u + (units - x) - 1;                  // the tile's last unit
+          const int owner = (int)(((last + 1) * ctas - 1) / total);    // the worker whose share holds it
+          it.n_parts = owner - me + 1;
+        }
+        u += take;
+        x += take;
+        if (x == units) {
+          x = 0;
+          if (++q == s.nq) q = 0, b = 0, ++kvh;
+        }
+        if (it.blk_hi > it.blk_lo) break;
       }
-      u += it.blk_hi - it.blk_lo;
     } else {
       const long long idx = u * all + ((u & 1) ? all - 1 - me : me);
       if (u * all >= (long long)s.nq * a.Hkv) return false;
@@ -182,10 +200,10 @@ struct ChunkWalk {
       it.kvh = (int)(idx / s.nq);
       q = (int)(idx - (long long)it.kvh * s.nq);
       it.part = -1, it.n_parts = 0;
+      it.b = chunk_find(s.first, a.B, q);
+      tile = q - s.first[it.b];
     }
-    it.b = chunk_find(s.first, a.B, q);
     const ChunkReq r = chunk_req(a, it.b, false);
-    const int tile = q - s.first[it.b];
     if (!s.shared_tiles) {
       it.nblk = chunk_tile_blocks(r, tile, TPT, KT);
       it.blk_lo = 0, it.blk_hi = it.nblk;
