@@ -64,6 +64,7 @@ struct FewSmem {
   alignas(1024) unsigned char ring[C::W][C::S][C::kSlot];
   float merge[C::W / 2][NT * (D / 16) * 4][32];          // O^T fragments of half of the warps
   float2 ml[C::W][NT * 8];
+  float2 row[NT * 8];                                    // maximum and sum over the warps
   alignas(8) uint64_t full[C::W][C::S];
   int poison[2], abort_flag;   // poison: by piece
   ChunkSched sched;
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
   volatile int* abort_flag = &sm.abort_flag;
   const int G = a.Hq / a.Hkv, TPT = kRows / G;
   constexpr int KT = kPageTokens;
+  const uint32_t g_inv = 65536u / G + 1;   // x / G = x * g_inv >> 16 for a tile's rows
 
   if (threadIdx.x == 0) {
     for (int w = 0; w < W; ++w)
@@ -164,6 +166,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
   // ---- the load stream: K and V of this warp's steps, piece after piece
   ChunkWalk lwalk;
   lwalk.begin(a, sm.sched, blockIdx.x, gridDim.x);
+  ChunkWalk walk = lwalk;
   ChunkItem lit;
   int ls = 0, lns = 0, lwin = -1, lpage = 0, ly = 0;
   uint32_t issued = 0, badmask = 0;   // slots armed; by slot: a bad page
@@ -217,8 +220,6 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
   for (int i = 0; i < S; ++i) issue();
 
   // ---- the pieces
-  ChunkWalk walk;
-  walk.begin(a, sm.sched, blockIdx.x, gridDim.x);
   ChunkItem it;
   uint32_t slot = 0, phase = 0, parity = 0;
   auto wait_slot = [&]() {
@@ -445,6 +446,17 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[nt][i][j] *= f, o[nt][i][j + 2] *= f;
       }
+    if (threadIdx.x < kRows) {
+      float mx = -INFINITY, total = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) mx = fmaxf(mx, sm.ml[w][threadIdx.x].x);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 v = sm.ml[w][threadIdx.x];
+        total += v.x == mx ? v.y : v.y * ex2(v.x - mx);
+      }
+      sm.row[threadIdx.x] = make_float2(mx, total);
+    }
     if (warp >= W / 2) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -464,45 +476,43 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
     }
     __syncthreads();
     const bool poison = sm.poison[parity] != 0;
-    if (threadIdx.x == 0) sm.poison[parity ^ 1] = 0;   // last read a piece ago, set again behind this piece's last barrier
-    for (int x = threadIdx.x; x < rows * (D / 2); x += W * 32) {
-      const int n = x / (D / 2), d = (x - n * (D / 2)) * 2, nt = n >> 3;
-      float mx = -INFINITY, total = 0.f;
+    // adds the non-finite values of the edge steps that token tok sees
+    auto seen_nonfinite = [&](int tok, int d, float (&y)[2]) {
+      const int from = max(it.blk_lo * KT, lim0 / kStep * kStep);
+      const int to = min(min(it.p0 + tok + 1, it.kv), it.blk_hi * KT);
+      for (int t = from; t < to; ++t) {
+        const int page = __ldg(a.page_table + (size_t)it.b * a.pt_stride + t / kPageTokens);
+        if (page < 0 || page >= a.num_pages) continue;
+        const size_t src = (((size_t)page * kPageTokens + t % kPageTokens) * a.Hkv + it.kvh) * D + d;
 #pragma unroll
-      for (int w = 0; w < W; ++w) mx = fmaxf(mx, sm.ml[w][n].x);
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float2 v = sm.ml[w][n];
-        total += v.x == mx ? v.y : v.y * ex2(v.x - mx);
+        for (int e = 0; e < 2; ++e) {
+          float v;
+          if constexpr (FP8) v = Elem<__nv_fp8_e4m3>::get(reinterpret_cast<const __nv_fp8_e4m3*>(a.v_pages), src + e);
+          else v = Elem<__nv_bfloat16>::get(reinterpret_cast<const __nv_bfloat16*>(a.v_pages), src + e);
+          if (!isfinite(v)) y[e] += v;
+        }
       }
+    };
+    if (threadIdx.x == 0) sm.poison[parity ^ 1] = 0;   // last read a piece ago, set again behind this piece's last barrier
+    // a thread keeps its pair of dimensions and walks over the rows
+    constexpr int RP = W * 32 / (D / 2);
+    const int d = (threadIdx.x % (D / 2)) * 2;
+#pragma unroll 8
+    for (int n = threadIdx.x / (D / 2); n < kRows; n += RP) {
+      if (n >= rows) break;
+      const float mx = sm.row[n].x, total = sm.row[n].y;
       float y[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int q = FP8 ? (d & 15) >> 1 : (d & 7) + e, hi = FP8 ? e : (d >> 3) & 1;
-        const int reg = (nt * MT + (d >> 4)) * 4 + hi * 2 + (n & 1), ln = q * 4 + ((n & 7) >> 1);
+        const int reg = ((n >> 3) * MT + (d >> 4)) * 4 + hi * 2 + (n & 1), ln = q * 4 + ((n & 7) >> 1);
         y[e] = 0.f;
 #pragma unroll
         for (int w = 0; w < W / 2; ++w) y[e] += sm.merge[w][reg][ln];
       }
-      const int tok = n / G;
-      if (total == 0.f) {
-        y[0] = y[1] = 0.f;
-      } else if (poison) {   // non-finite values of the edge steps that this row sees
-        const int from = max(it.blk_lo * KT, lim0 / kStep * kStep);
-        const int to = min(min(it.p0 + tok + 1, it.kv), it.blk_hi * KT);
-        for (int t = from; t < to; ++t) {
-          const int page = __ldg(a.page_table + (size_t)it.b * a.pt_stride + t / kPageTokens);
-          if (page < 0 || page >= a.num_pages) continue;
-          const size_t src = (((size_t)page * kPageTokens + t % kPageTokens) * a.Hkv + it.kvh) * D + d;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v;
-            if constexpr (FP8) v = Elem<__nv_fp8_e4m3>::get(reinterpret_cast<const __nv_fp8_e4m3*>(a.v_pages), src + e);
-            else v = Elem<__nv_bfloat16>::get(reinterpret_cast<const __nv_bfloat16*>(a.v_pages), src + e);
-            if (!isfinite(v)) y[e] += v;
-          }
-        }
-      }
+      const int tok = (int)((uint32_t)n * g_inv >> 16);
+      if (total == 0.f) y[0] = y[1] = 0.f;
+      else if (poison) seen_nonfinite(tok, d, y);
       if (it.part < 0) {
         const float inv = total == 0.f ? 0.f : vmul / total;
         const size_t row = (size_t)(it.t0 + tok) * a.Hq + it.kvh * G + (n - tok * G);

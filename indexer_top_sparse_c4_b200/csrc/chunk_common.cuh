@@ -154,9 +154,16 @@ struct ChunkWalk {
       total = (long long)wq * a.Hkv;
       if (total < ctas) ctas = (int)total;
       if (me < ctas) {
-        u = total * me / ctas;
-        u1 = total * (me + 1) / ctas;
-        kvh = (int)(u / wq);
+        if (total < (1 << 23)) {   // 32-bit divisions are several times cheaper
+          const uint32_t t = (uint32_t)total;
+          u = t * (uint32_t)me / (uint32_t)ctas;
+          u1 = t * (uint32_t)(me + 1) / (uint32_t)ctas;
+          kvh = (int)((uint32_t)u / (uint32_t)wq);
+        } else {
+          u = total * me / ctas;
+          u1 = total * (me + 1) / ctas;
+          kvh = (int)(u / wq);
+        }
         const int y = (int)(u - (long long)kvh * wq);
         q = chunk_find(s.blk, s.nq, y);
         x = y - s.blk[q];
@@ -181,7 +188,9 @@ struct ChunkWalk {
         } else if (it.blk_hi < nblk) {
           it.part = 2 * me + 1;
           const long long last = u + (units - x) - 1;                  // the tile's last unit
-          const int owner = (int)(((last + 1) * ctas - 1) / total);    // the worker whose share holds it
+          // the worker whose share holds it
+          const int owner = total < (1 << 23) ? (int)(((uint32_t)(last + 1) * (uint32_t)ctas - 1) / (uint32_t)total)
+                                              : (int)(((last + 1) * ctas - 1) / total);
           it.n_parts = owner - me + 1;
         }
         u += take;
