@@ -16,38 +16,29 @@
 // the product is formed in 64 bits (exact: 31 + 24 bits), divided by 2 pi and
 // reduced to a fraction of a turn there; sine and cosine of the fraction (at
 // most half a turn, in 32 bits) are then good to a few units of 2^-24.
-// One thread per (token, frequency) computes them once for all heads.
 //
 // Bound: HBM for a prefill chunk (each value is read and written once), the
-// launch for a decode step.  A thread moves 16-byte vectors of 8 BF16 values
-// (two of them for F32), a warp whole heads; a rotated pair of vectors is
-// read and written by the same thread, so the queries may be rotated in place.
+// launch for a decode step.  A warp takes a token, or with few tokens a part
+// of its heads, and waits for no other: it forms the token's angles once
+// (shared memory, then registers) and walks over the heads, D / 16 lanes to a
+// head and two 16-byte vectors of a rotated pair to a lane, the next heads'
+// loads in flight.  Measured (8,192 tokens, 24/2 heads of D 256, BF16): 44 us,
+// 5.3 TB/s; one CTA per four tokens with the angles read from shared memory
+// for every head took 60 us (eight lanes to a bank), and four heads in flight
+// at twice the registers 57 us.  A rotated pair is read and written by the
+// same lane, so the queries may be rotated in place.
 #include "qsa_internal.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxHalf = 128;
+constexpr int kWarps = 4736;   // warps a call is spread over, if its heads are enough (32 per SM)
 
 struct Vec8 {
   float v[8];
 };
-__device__ __forceinline__ Vec8 load8(const float* p) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  return Vec8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-}
-__device__ __forceinline__ Vec8 load8(const __nv_bfloat16* p) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-  Vec8 r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    r.v[2 * j] = __uint_as_float(w[j] << 16);
-    r.v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-  }
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -84,115 +75,167 @@ __device__ __forceinline__ int axis_of(const RopeArgs& a, int i) {
   return i < a.sec0 ? 0 : i < a.sec0 + a.sec1 ? 1 : 2;
 }
 
-// One head of one token: `unit` is the thread's piece of it.  Units of a head
-// with pairs in halves: half/8 pairs of vectors, then the vectors behind
-// rot_dim; with adjacent pairs: every vector.
-template <bool ADJ, typename XT, typename OT>
-__device__ __forceinline__ void head_unit(const XT* src, OT* dst, int unit, int rot, const float2* cs, float scale) {
-  if constexpr (ADJ) {
-    Vec8 x = load8(src + unit * 8);
-    if (unit * 8 < rot) {
+__device__ __forceinline__ void turn_adjacent(Vec8& x, const float2* cs) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 c = cs[unit * 4 + j];
-        const float p = x.v[2 * j], q = x.v[2 * j + 1];
-        x.v[2 * j] = p * c.x - q * c.y;
-        x.v[2 * j + 1] = q * c.x + p * c.y;
-      }
-    }
-    store8(dst + unit * 8, x, scale);
-  } else {
-    const int half = rot >> 1, pairs = half >> 3;
-    if (unit < pairs) {
-      Vec8 x = load8(src + unit * 8), y = load8(src + half + unit * 8);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 c = cs[unit * 8 + j];
-        const float p = x.v[j], q = y.v[j];
-        x.v[j] = p * c.x - q * c.y;
-        y.v[j] = q * c.x + p * c.y;
-      }
-      store8(dst + unit * 8, x, scale);
-      store8(dst + half + unit * 8, y, scale);
-    } else {
-      const int off = rot + (unit - pairs) * 8;
-      store8(dst + off, load8(src + off), scale);
-    }
+  for (int e = 0; e < 4; ++e) {
+    const float p = x.v[2 * e], r = x.v[2 * e + 1];
+    x.v[2 * e] = p * cs[e].x - r * cs[e].y;
+    x.v[2 * e + 1] = r * cs[e].x + p * cs[e].y;
   }
 }
 
+// What a lane holds of one head of one token: two vectors of 8.
+template <typename XT>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 a[2], b[2];
+  __device__ __forceinline__ void load(const float* p, const float* q) {
+    a[0] = *reinterpret_cast<const float4*>(p), a[1] = *(reinterpret_cast<const float4*>(p) + 1);
+    b[0] = *reinterpret_cast<const float4*>(q), b[1] = *(reinterpret_cast<const float4*>(q) + 1);
+  }
+  static __device__ __forceinline__ Vec8 vec(const float4 (&v)[2]) {
+    return Vec8{{v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w}};
+  }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 a[1], b[1];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+    a[0] = *reinterpret_cast<const uint4*>(p);
+    b[0] = *reinterpret_cast<const uint4*>(q);
+  }
+  static __device__ __forceinline__ Vec8 vec(const uint4 (&v)[1]) {
+    const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+    Vec8 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r.v[2 * j] = __uint_as_float(w[j] << 16);
+      r.v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+    return r;
+  }
+};
+
 template <bool ADJ, typename XT, typename KVT>
-__global__ void __launch_bounds__(kThreads) rope_write_kernel(RopeArgs a, int tok_per_cta, int lanes_log2) {
-  extern __shared__ float2 cs_smem[];  // [tok_per_cta][half] (cos, sin)
-  __shared__ int slots[32];
-  const int tid = threadIdx.x, half = a.rot_dim >> 1;
-  const int t0 = blockIdx.x * tok_per_cta;
-  const int ntok = min(tok_per_cta, a.T - t0);
+__global__ void __launch_bounds__(kThreads, 6) rope_write_kernel(RopeArgs a, int parts, int part_heads, int lanes_log2) {
+  constexpr int kAhead = sizeof(XT) == 2 ? 3 : 2;   // heads whose loads a lane has in flight
+  __shared__ float2 cs_smem[kThreads / 32][kMaxHalf];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = a.rot_dim >> 1;
+  const int w = blockIdx.x * (kThreads / 32) + warp, t = w / parts, part = w - t * parts;
   pdl_wait();
   pdl_launch_dependents();
-  if (tid < ntok) {
-    int s = a.slot[t0 + tid];
-    if (s < -1 || s >= a.num_pages * (long long)kPageTokens) {
-      flag(a.status, QSA_DEV_BAD_PAGE);
-      s = -1;
-    }
-    slots[tid] = s;
+  if (t >= a.T) return;                // whole warps; none waits for another
+  int slot = a.slot[t];
+  if (slot < -1 || slot >= a.num_pages * (long long)kPageTokens) {
+    if (lane == 0) flag(a.status, QSA_DEV_BAD_PAGE);
+    slot = -1;
   }
-  for (int i = tid; i < ntok * half; i += kThreads) {
-    const int t = i / half, f = i - t * half;
-    const double angle = (double)a.pos[(size_t)axis_of(a, f) * a.pos_stride + t0 + t] * (double)a.inv_freq[f];
+  if (slot < 0) return;
+  // D / 16 lanes to a head, two vectors of 8 to a lane: the two of a pair, or
+  // two of those behind rot_dim; with adjacent pairs, and for values, vector
+  // `unit` of either half
+  const int lanes = a.D >> 4, unit = lane & (lanes - 1), groups = 32 >> lanes_log2;
+  const int h_end = min(a.Hq + 2 * a.Hkv, (part + 1) * part_heads);
+  const int pairs = half >> 3, voff0 = unit * 8, voff1 = voff0 + (a.D >> 1);
+  int off0 = voff0, off1 = voff1;
+  if (!ADJ) {
+    if (unit < pairs) off1 = half + unit * 8;
+    else off0 = a.rot_dim + (unit - pairs) * 8, off1 = off0 + ((a.D - a.rot_dim) >> 1);
+  }
+
+  // a group of 2^lanes_log2 lanes per head, query heads first, then keys, then
+  // values; the loads of kAhead heads are in flight at a time
+  const XT* q = reinterpret_cast<const XT*>(a.q) + (size_t)t * a.q_stride;
+  const XT* k = reinterpret_cast<const XT*>(a.k) + (size_t)t * a.k_stride;
+  const XT* v = reinterpret_cast<const XT*>(a.v) + (size_t)t * a.v_stride;
+  XT* q_out = reinterpret_cast<XT*>(a.q_out) + (size_t)t * a.Hq * a.D;
+  KVT* kc = reinterpret_cast<KVT*>(a.k_pages) + (size_t)slot * a.Hkv * a.D;
+  KVT* vc = reinterpret_cast<KVT*>(a.v_pages) + (size_t)slot * a.Hkv * a.D;
+  auto fetch = [&](int h, Raw<XT>& x) {
+    if (h >= h_end) return;
+    if (h < a.Hq + a.Hkv) {
+      const XT* src = h < a.Hq ? q + h * a.D : k + (h - a.Hq) * a.D;
+      x.load(src + off0, src + off1);
+    } else {
+      const XT* src = v + (h - a.Hq - a.Hkv) * a.D;
+      x.load(src + voff0, src + voff1);
+    }
+  };
+  int hb = part * part_heads + (lane >> lanes_log2);
+  Raw<XT> x[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) fetch(hb + j * groups, x[j]);   // in flight while the angles are formed
+
+  // (cos, sin) of frequency f at [f % NF][f / NF], NF of them a thread: read
+  // back without bank conflicts, and kept in registers for all heads
+  constexpr int NF = ADJ ? 4 : 8;
+  const int fu = half / NF;
+  for (int f = lane; f < half; f += 32) {
+    const double angle = (double)a.pos[(size_t)axis_of(a, f) * a.pos_stride + t] * (double)a.inv_freq[f];
     const double turns = angle * 0.15915494309189533577;  // 1 / (2 pi)
     float s, c;
     sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-    cs_smem[i] = make_float2(c * a.rot_scale, s * a.rot_scale);
+    cs_smem[warp][(f % NF) * fu + f / NF] = make_float2(c * a.rot_scale, s * a.rot_scale);
   }
-  __syncthreads();
-
-  // a group of 2^lanes_log2 threads per head, query heads first, then keys, then values
-  const int units = ADJ ? a.D >> 3 : (half >> 3) + ((a.D - a.rot_dim) >> 3);
-  const int lanes = 1 << lanes_log2, unit = tid & (lanes - 1);
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int groups = kThreads >> lanes_log2;
-  const XT* q = reinterpret_cast<const XT*>(a.q);
-  const XT* k = reinterpret_cast<const XT*>(a.k);
-  const XT* v = reinterpret_cast<const XT*>(a.v);
-  XT* q_out = reinterpret_cast<XT*>(a.q_out);
-  KVT* kc = reinterpret_cast<KVT*>(a.k_pages);
-  KVT* vc = reinterpret_cast<KVT*>(a.v_pages);
-  for (int i = tid >> lanes_log2; i < ntok * heads; i += groups) {
-    const int t = i / heads, h = i - t * heads;
-    const int slot = slots[t];
-    if (slot < 0) continue;
-    const size_t tt = (size_t)(t0 + t);
-    const float2* cs = cs_smem + t * half;
-    if (h < a.Hq) {
-      if (unit < units)
-        head_unit<ADJ>(q + tt * a.q_stride + (size_t)h * a.D, q_out + (tt * a.Hq + h) * a.D, unit, a.rot_dim, cs, 1.f);
-    } else if (h < a.Hq + a.Hkv) {
-      const int kh = h - a.Hq;
-      if (unit < units)
-        head_unit<ADJ>(k + tt * a.k_stride + (size_t)kh * a.D, kc + ((size_t)slot * a.Hkv + kh) * a.D, unit, a.rot_dim,
-                       cs, a.k_scale);
-    } else {
-      const int vh = h - a.Hq - a.Hkv;
-      const XT* src = v + tt * a.v_stride + (size_t)vh * a.D;
-      KVT* dst = vc + ((size_t)slot * a.Hkv + vh) * a.D;
-      for (int u = unit; u < (a.D >> 3); u += lanes) store8(dst + u * 8, load8(src + u * 8), a.v_scale);
+  __syncwarp();
+  float2 cs[8];                        // adjacent pairs: four of each vector
+  const bool turn0 = unit < fu, turn1 = ADJ && unit + lanes < fu;
+#pragma unroll
+  for (int j = 0; j < NF; ++j) {
+    if (turn0) cs[j] = cs_smem[warp][j * fu + unit];
+    if (turn1) cs[4 + j % 4] = cs_smem[warp][j * fu + unit + lanes];
+  }
+  for (;;) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {   // slot j is refilled as soon as its head has been taken from it
+      const int h = hb + j * groups;
+      if (h >= h_end) return;
+      Vec8 y = Raw<XT>::vec(x[j].a), z = Raw<XT>::vec(x[j].b);
+      fetch(h + kAhead * groups, x[j]);
+      if (h < a.Hq + a.Hkv) {
+        if constexpr (ADJ) {
+          if (turn0) turn_adjacent(y, cs);
+          if (turn1) turn_adjacent(z, cs + 4);
+        } else if (turn0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float p = y.v[e], r = z.v[e];
+            y.v[e] = p * cs[e].x - r * cs[e].y;
+            z.v[e] = r * cs[e].x + p * cs[e].y;
+          }
+        }
+        if (h < a.Hq) {
+          store8(q_out + h * a.D + off0, y, 1.f);
+          store8(q_out + h * a.D + off1, z, 1.f);
+        } else {
+          KVT* dst = kc + (h - a.Hq) * a.D;
+          store8(dst + off0, y, a.k_scale);
+          store8(dst + off1, z, a.k_scale);
+        }
+      } else {
+        KVT* dst = vc + (h - a.Hq - a.Hkv) * a.D;
+        store8(dst + voff0, y, a.v_scale);
+        store8(dst + voff1, z, a.v_scale);
+      }
     }
+    hb += kAhead * groups;
   }
 }
 
 template <bool ADJ, typename XT, typename KVT>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
-  const int half = a.rot_dim >> 1;
-  const int units = ADJ ? a.D >> 3 : (half >> 3) + ((a.D - a.rot_dim) >> 3);
-  int lg = 0;
-  while ((1 << lg) < units) ++lg;
-  // few tokens: one per CTA, so that a step spreads over the SMs; many: four
-  // share a CTA's set-up
-  const int per = a.T <= 148 * 8 ? 1 : 4;
-  return launch_k(rope_write_kernel<ADJ, XT, KVT>, dim3((a.T + per - 1) / per), dim3(kThreads),
-                  (size_t)per * half * sizeof(float2), s, 1, a, per, lg);
+  const int lg = a.D == 64 ? 2 : a.D == 128 ? 3 : 4;
+  // a warp per token, or, with few tokens, per part of a token's heads: a
+  // whole pass of the warp's groups at least, and as many warps as 148 SMs hold
+  const int heads = a.Hq + 2 * a.Hkv, groups = 32 >> lg;
+  const int want = (kWarps + a.T - 1) / a.T;
+  const int part_heads = (heads + want - 1) / want > groups ? ((heads + want - 1) / want + groups - 1) / groups * groups : groups;
+  const int parts = (heads + part_heads - 1) / part_heads;
+  const long long warps = (long long)a.T * parts;
+  const int per = kThreads / 32;
+  return launch_k(rope_write_kernel<ADJ, XT, KVT>, dim3((unsigned)((warps + per - 1) / per)), dim3(kThreads), 0, s, 1, a,
+                  parts, part_heads, lg);
 }
 template <bool ADJ, typename XT>
 cudaError_t launch_kv(const RopeArgs& a, cudaStream_t s) {

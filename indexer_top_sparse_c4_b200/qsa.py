@@ -484,32 +484,33 @@ def _device(anchor) -> int:
     return anchor.get_device()
 
 
-def _pointers(dev, names, tensors):
-    """Addresses of contiguous tensors on device dev (None stays None)."""
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != dev:
-            raise ValueError(f"{names.split()[len(out)]} is on {t.device}, the call runs on cuda:{dev}")
-        if not t.is_contiguous():
-            raise ValueError(f"{names.split()[len(out)]}: libqsa takes contiguous tensors")
-        out.append(t.data_ptr())
-    return out
+def _address(dev, t):
+    """Address of a contiguous tensor on device dev, or None."""
+    if t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"a tensor is on {t.device}, the call runs on cuda:{dev}")
+    raise ValueError("libqsa takes contiguous tensors")
+
+
+def _pointers(dev, *tensors):
+    return [None if t is None else t.data_ptr() if t.get_device() == dev and t.is_contiguous() else _address(dev, t)
+            for t in tensors]
 
 
 _i32 = torch.int32
 
 
-def _int32(names, tensors):
-    for i, t in enumerate(tensors):
+def _int32(names, *tensors):
+    for t in tensors:
         if t.dtype is not _i32:
-            raise TypeError(f"{names.split()[i]} must be int32 (got {t.dtype})")
+            raise TypeError(f"{names} must be int32 (got {t.dtype})")
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+# the bindings behind torch.cuda.current_stream and current_device, without their objects
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _DTYPES = {torch.float32: QSA_F32, torch.bfloat16: QSA_BF16, torch.float8_e4m3fn: QSA_FP8_E4M3,
            torch.uint8: QSA_FP8_E4M3}
 
@@ -525,7 +526,7 @@ def _call(fn, dev, stream, *args):
     """One library call on the device of its tensors, whichever is current;
     stream None: that device's current stream."""
     s = _raw_stream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -540,19 +541,19 @@ def qsa_chunk_plan(n_cached, n_new, free_pages, page_table, num_pages, cu_new, k
     tensors int32; T = the size of q_req, q_pos and slot).  Fills cu_new
     [B + 1], kv_len [B], q_req / q_pos / slot [T] (-1 behind the last token),
     n_taken [1] and the new entries of page_table."""
-    names = "n_cached n_new free_pages page_table cu_new kv_len q_req q_pos slot n_taken dev_status"
-    tensors = (n_cached, n_new, free_pages, page_table, cu_new, kv_len, q_req, q_pos, slot, n_taken)
     B, T = n_cached.numel(), slot.numel()
-    _int32(names, tensors)
+    _int32("the lengths, pages, tables and maps", n_cached, n_new, free_pages, page_table, cu_new, kv_len, q_req, q_pos,
+           slot, n_taken)
+    shape = page_table.shape
     if (n_new.numel() != B or kv_len.numel() != B or cu_new.numel() != B + 1 or q_req.numel() != T
-            or q_pos.numel() != T or n_taken.numel() < 1 or page_table.dim() != 2):
+            or q_pos.numel() != T or n_taken.numel() < 1 or len(shape) != 2):
         raise ValueError("shapes: n_cached, n_new, kv_len [B], cu_new [B + 1], q_req, q_pos, slot [T], n_taken [1], "
                          "page_table [pt_rows, pt_stride]")
     dev = _device(page_table)
-    p = _pointers(dev, names, (*tensors, dev_status))
-    rows, width = page_table.shape
-    _call(lib().qsa_chunk_plan, dev, stream, p[0], p[1], B, p[2], free_pages.numel(), p[3], rows, width, int(num_pages),
-          T, *p[4:])
+    old, new, free, table, *out = _pointers(dev, n_cached, n_new, free_pages, page_table, cu_new, kv_len, q_req, q_pos,
+                                            slot, n_taken, dev_status)
+    _call(lib().qsa_chunk_plan, dev, stream, old, new, B, free, free_pages.numel(), table, shape[0], shape[1],
+          num_pages, T, *out)
     return cu_new, kv_len, q_req, q_pos, slot, n_taken
 
 
@@ -591,7 +592,7 @@ def qsa_rope_write(q, k, v, pos, inv_freq, slot, q_out, k_pages, v_pages, sectio
     sec = (half, 0, 0) if sections is None else (*sections, *(0,) * (3 - len(sections)))
     if len(sec) != 3 or not 1 <= axes <= 3:
         raise ValueError("one to three axes and sections")
-    _int32("pos slot", (pos, slot))
+    _int32("pos and slot", pos, slot)
     if ps[-1] != T or slot.numel() != T or len(ps) > 2:
         raise ValueError(f"pos must be [{T}] or [n_axes, {T}], slot [{T}]")
     if T > 1 and pos.stride(-1) != 1:
@@ -611,8 +612,7 @@ def qsa_rope_write(q, k, v, pos, inv_freq, slot, q_out, k_pages, v_pages, sectio
     _device(k_pages)
     if pos.get_device() != dev:
         raise ValueError(f"pos is on {pos.device}, the call runs on cuda:{dev}")
-    freq_p, slot_p, out_p, k_p, v_p, st_p = _pointers(dev, "inv_freq slot q_out k_pages v_pages dev_status",
-                                                      (inv_freq, slot, q_out, k_pages, v_pages, dev_status))
+    freq_p, slot_p, out_p, k_p, v_p, st_p = _pointers(dev, inv_freq, slot, q_out, k_pages, v_pages, dev_status)
     _call(lib().qsa_rope_write, dev, stream, qp, qs, kp, ks, vp, vs, x_dt, pos.data_ptr(), axes,
           pos.stride(0) if axes > 1 else T, *sec, 1 if interleaved_axes else 0, 1 if adjacent_pairs else 0, freq_p,
           2 * half, rot_scale, slot_p, T, Hq, Hkv, D, out_p, k_p, v_p, kv_dt, k_scale, v_scale, num_pages, st_p)
@@ -633,7 +633,7 @@ def qsa_chunk_attn(q, k_pages, v_pages, page_table, cu_new, kv_len, out, workspa
     cu_new[b+1] - 1 of q [T, Hq, D]) over its kv_len[b] cached tokens."""
     T, Hq, D = q.shape
     B = kv_len.numel()
-    _int32("page_table cu_new kv_len", (page_table, cu_new, kv_len))
+    _int32("page_table, cu_new and kv_len", page_table, cu_new, kv_len)
     if k_pages.dim() != 4:
         raise ValueError("k_pages and v_pages must be [num_pages, 64, Hkv, D]")
     Hkv = k_pages.shape[2]
@@ -647,8 +647,7 @@ def qsa_chunk_attn(q, k_pages, v_pages, page_table, cu_new, kv_len, out, workspa
     q_dt, kv_dt = _code(q), _code(k_pages)
     dev = _device(q)
     q_p, k_p, v_p, pt_p, cu_p, kv_p, out_p, lse_p, ws_p, st_p = _pointers(
-        dev, "q k_pages v_pages page_table cu_new kv_len out lse workspace dev_status",
-        (q, k_pages, v_pages, page_table, cu_new, kv_len, out, lse, workspace, dev_status))
+        dev, q, k_pages, v_pages, page_table, cu_new, kv_len, out, lse, workspace, dev_status)
     rows, width = page_table.shape
     _call(lib().qsa_chunk_attn, dev, stream, q_p, q_dt, k_p, v_p, kv_dt, k_scale, v_scale, num_pages, pt_p, rows, width,
           cu_p, kv_p, B, T, Hq, Hkv, D, sm_scale, out_p, lse_p, ws_p,
