@@ -11,9 +11,10 @@
 // the choice between the general and the tensor-core kernel.
 //
 // General kernel: a CTA takes a tile of 32 query rows (whole tokens: all query
-// heads of one KV head) against one page of 64 keys at a time.  128 threads
-// hold 4 x 4 logits each; the page's keys and values go through shared memory
-// in FP32 and are read back as float4 (64 multiply-adds per 8 shared loads),
+// heads of one KV head) against one page of 64 keys at a time.  256 threads
+// hold 2 x 4 logits each (128 of 4 x 4 share loads better, but leave a
+// scheduler one warp to hide latencies with); the page's keys and values go through shared memory
+// in FP32 and are read back as float4 (32 multiply-adds per 6 shared loads),
 // the running maximum and sum of the softmax stay in registers, 16 threads to
 // a row.  It is bound by the FP32 pipes and serves float32 models, whose
 // values the tensor cores would round.
@@ -37,7 +38,8 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int kR = 2;                  // query rows of a thread
 constexpr int kRows = 32;              // query rows of a tile
 constexpr int kKeys = kPageTokens;     // keys of a block: one page
 
@@ -60,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
   pdl_wait();
   pdl_launch_dependents();
   if (tid == 0 && blockIdx.x < kChunkMaxCtas) ws.desc[blockIdx.x].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, kKeys, gridDim.x, false, 1);
+  chunk_sched_build(a, sm.sched, TPT, kKeys, blockIdx.x, gridDim.x, false, 1);
   ChunkWalk walk;
   walk.begin(a, sm.sched, blockIdx.x, gridDim.x);
   const QT* q = reinterpret_cast<const QT*>(a.q);
@@ -80,11 +82,11 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
 #pragma unroll
       for (int j = 0; j < 4; ++j) sm.q[r][d + j] = x[j] * qk_scale_log2;
     }
-    int lim[4];                        // keys each of this thread's rows sees
-    float m[4], l[4], o[4][C4 * 4];
+    int lim[kR];                        // keys each of this thread's rows sees
+    float m[kR], l[kR], o[kR][C4 * 4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = rg * 4 + i;
+    for (int i = 0; i < kR; ++i) {
+      const int r = rg * kR + i;
       lim[i] = r < rows ? min(it.p0 + r / G + 1, it.kv) : it.kv;   // rows past the tile are not stored
       m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
@@ -113,16 +115,16 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
       }
       __syncthreads();
       // logits (base 2) of rows rg*4.., keys cg + 16 j
-      float s[4][4] = {};
+      float s[kR][4] = {};
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
-        float4 x[4], y[4];
+        float4 x[kR], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(&sm.q[rg * 4 + i][d]);
+        for (int i = 0; i < kR; ++i) x[i] = *reinterpret_cast<const float4*>(&sm.q[rg * kR + i][d]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(&sm.k[cg + 16 * j][d]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kR; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
       }
       bool whole = page >= 0;          // every row sees every key of the page
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kR; ++i) {
         const int seen = page >= 0 ? lim[i] - key0 : 0;
         whole = whole && seen >= kKeys;
         float mx = m[i];
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
         for (int j = 0; j < 4; ++j) {
           const float e = exp2f(s[i][j] - base);
           sum += e;
-          sm.p[rg * 4 + i][cg + 16 * j] = e;
+          sm.p[rg * kR + i][cg + 16 * j] = e;
         }
 #pragma unroll
         for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -163,14 +165,14 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
       __syncwarp();                    // a row's 16 threads share a warp
       if (page >= 0) {
         for (int j = 0; j < live; ++j) {
-          float p[4];
+          float p[kR];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = sm.p[rg * 4 + i][j];
+          for (int i = 0; i < kR; ++i) p[i] = sm.p[rg * kR + i][j];
 #pragma unroll
           for (int c = 0; c < C4; ++c) {
             const float4 y = *reinterpret_cast<const float4*>(&sm.v[j][cg * 4 + 64 * c]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kR; ++i) {
               // a value a row does not see must not reach it, not even as 0 * inf
               if (whole || key0 + j < lim[i]) {
                 o[i][4 * c] = fmaf(p[i], y.x, o[i][4 * c]);
@@ -184,8 +186,8 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = rg * 4 + i;
+    for (int i = 0; i < kR; ++i) {
+      const int r = rg * kR + i;
       if (r >= rows) continue;
       if (it.part < 0) {
         const size_t row = (size_t)(it.t0 + r / G) * a.Hq + it.kvh * G + r % G;

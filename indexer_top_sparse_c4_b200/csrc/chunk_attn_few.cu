@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) ws.desc[blockIdx.x].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, KT, gridDim.x, true, kLead);
+  chunk_sched_build(a, sm.sched, TPT, KT, blockIdx.x, gridDim.x, true, kLead);
 
   // Keys this tile's last row sees, and the steps of a piece that hold any.
   auto steps_of = [&](const ChunkItem& x) {

@@ -315,15 +315,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();          // the pair's barriers are initialised
-  tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0 && rank == 0) ws.desc[worker].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, kKeys, workers, false, kLead);
+  chunk_sched_build(a, sm.sched, TPT, kKeys, worker, workers, false, kLead);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();          // the pair's barriers are initialised, its TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
   ChunkWalk walk;
   walk.begin(a, sm.sched, worker, workers);
   ChunkItem it;

@@ -57,6 +57,9 @@ struct ChunkSched {
   int blk[kChunkMaxTiles + 1];    // shared tiles: units before each query tile (its lead and its key blocks)
   int warp_sum[32];
   int nq, shared_tiles, lead;
+  // shared tiles: where this worker starts and ends, and its first tile
+  long long u, u1;
+  int ctas, kvh, q, x, b;         // ctas: workers that have work; x: unit within the tile; b: request
 };
 
 // Exclusive prefix sum of v over the CTA's threads plus `carry`; returns this
@@ -100,9 +103,10 @@ __device__ __forceinline__ int chunk_find(const int* v, int n, int x) {
   return lo;
 }
 
-// Called by every thread of the CTA; the table is ready on return.  share: tiles
-// are split over workers however many there are (as far as the table holds them).
-__device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched& s, int TPT, int KT, int workers,
+// Called by every thread of the CTA for worker `me` of `all` (a CTA, or a pair
+// of them); the table is ready on return.  share: tiles are split over workers
+// however many there are (as far as the table holds them).
+__device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched& s, int TPT, int KT, int me, int all,
                                                   bool share, int lead) {
   int carry = 0;
   for (int base = 0; base < a.B; base += blockDim.x) {
@@ -112,29 +116,57 @@ __device__ __forceinline__ void chunk_sched_build(const ChunkArgs& a, ChunkSched
     const int before = chunk_scan(n, s.warp_sum, carry);
     if (b < a.B) s.first[b] = before;
   }
+  const int nq = carry;
+  const bool shared = nq <= kChunkMaxTiles && (share || (long long)nq * a.Hkv < 4ll * all);
   if (threadIdx.x == 0) {
-    s.first[a.B] = carry;
-    s.nq = carry;
+    s.first[a.B] = nq;
+    s.nq = nq;
     s.lead = lead;
-    s.shared_tiles = carry <= kChunkMaxTiles && (share || (long long)carry * a.Hkv < 4ll * workers);
+    s.shared_tiles = shared;
+    s.u = s.u1 = 0;
+    s.ctas = all;
   }
   __syncthreads();
-  if (s.shared_tiles) {
-    const int nq = s.nq;
-    carry = 0;
-    for (int base = 0; base < nq; base += blockDim.x) {
-      const int q = base + threadIdx.x;
-      int n = 0;
-      if (q < nq) {
-        const int b = chunk_find(s.first, a.B, q);
-        n = lead + chunk_tile_blocks(chunk_req(a, b, false), q - s.first[b], TPT, KT);
-      }
-      const int before = chunk_scan(n, s.warp_sum, carry);
-      if (q < nq) s.blk[q] = before;
+  if (!shared || nq == 0) return;
+  carry = 0;
+  for (int base = 0; base < nq; base += blockDim.x) {
+    const int q = base + threadIdx.x;
+    int n = 0;
+    if (q < nq) {
+      const int b = chunk_find(s.first, a.B, q);
+      n = lead + chunk_tile_blocks(chunk_req(a, b, false), q - s.first[b], TPT, KT);
     }
-    if (threadIdx.x == 0) s.blk[nq] = carry;
-    __syncthreads();
+    const int before = chunk_scan(n, s.warp_sum, carry);
+    if (q < nq) s.blk[q] = before;
   }
+  if (threadIdx.x == 0) s.blk[nq] = carry;
+  __syncthreads();
+  const int wq = carry;
+  const long long total = (long long)wq * a.Hkv;
+  const int ctas = total < all ? (int)total : all;
+  long long u = 0, u1 = 0;
+  int kvh = 0;
+  if (me < ctas) {
+    if (total < (1 << 23)) {   // 32-bit divisions are several times cheaper
+      const uint32_t t = (uint32_t)total;
+      u = t * (uint32_t)me / (uint32_t)ctas;
+      u1 = t * (uint32_t)(me + 1) / (uint32_t)ctas;
+      kvh = (int)((uint32_t)u / (uint32_t)wq);
+    } else {
+      u = total * me / ctas;
+      u1 = total * (me + 1) / ctas;
+      kvh = (int)(u / wq);
+    }
+  }
+  // the thread whose tile holds the first unit writes the start down
+  const int y = (int)(u - (long long)kvh * wq);
+  for (int q = threadIdx.x; q < nq; q += blockDim.x) {
+    if (s.blk[q] <= y && y < s.blk[q + 1]) {
+      s.u = u, s.u1 = u1, s.ctas = ctas, s.kvh = kvh;
+      s.q = q, s.x = y - s.blk[q], s.b = chunk_find(s.first, a.B, q);
+    }
+  }
+  __syncthreads();
 }
 
 // The walk of worker `me` of `all` (a CTA, or a pair of them) over its pieces;
@@ -147,28 +179,11 @@ struct ChunkWalk {
 
   __device__ __forceinline__ void begin(const ChunkArgs& a, const ChunkSched& s, int me_, int all_) {
     me = me_, all = all_;
-    u = 0, u1 = 0, total = 0, ctas = all;
+    u = s.u, u1 = s.u1, ctas = s.ctas, total = 0;
     kvh = q = x = b = 0;
-    if (s.shared_tiles) {
-      const int wq = s.blk[s.nq];
-      total = (long long)wq * a.Hkv;
-      if (total < ctas) ctas = (int)total;
-      if (me < ctas) {
-        if (total < (1 << 23)) {   // 32-bit divisions are several times cheaper
-          const uint32_t t = (uint32_t)total;
-          u = t * (uint32_t)me / (uint32_t)ctas;
-          u1 = t * (uint32_t)(me + 1) / (uint32_t)ctas;
-          kvh = (int)((uint32_t)u / (uint32_t)wq);
-        } else {
-          u = total * me / ctas;
-          u1 = total * (me + 1) / ctas;
-          kvh = (int)(u / wq);
-        }
-        const int y = (int)(u - (long long)kvh * wq);
-        q = chunk_find(s.blk, s.nq, y);
-        x = y - s.blk[q];
-        b = chunk_find(s.first, a.B, q);
-      }
+    if (s.shared_tiles && s.nq > 0) {
+      total = (long long)s.blk[s.nq] * a.Hkv;
+      kvh = s.kvh, q = s.q, x = s.x, b = s.b;
     }
   }
   __device__ __forceinline__ bool next(const ChunkArgs& a, const ChunkSched& s, int TPT, int KT, ChunkItem& it) {
