@@ -206,6 +206,26 @@ __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// two FP32 operations an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t x, y, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -602,15 +622,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           }
           const float neg = m == -INFINITY ? 0.f : -m;
           uint32_t p[32];
-          float s0 = 0.f, s1 = 0.f;
+          const float2 sc2 = make_float2(sc, sc), neg2 = make_float2(neg, neg);
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float x = ex2(fmaf(s[2 * i], sc, neg)), y = ex2(fmaf(s[2 * i + 1], sc, neg));
-            s0 += x;
-            s1 += y;
-            p[i] = pack16<FP8>(x, y);
+          for (int i = 0; i < 32; i += 2) {
+            float2 x = fma2(make_float2(s[2 * i], s[2 * i + 1]), sc2, neg2);
+            float2 y = fma2(make_float2(s[2 * i + 2], s[2 * i + 3]), sc2, neg2);
+            x.x = ex2(x.x), x.y = ex2(x.y), y.x = ex2(y.x), y.y = ex2(y.y);
+            sum0 = add2(sum0, x);
+            sum1 = add2(sum1, y);
+            p[i] = pack16<FP8>(x.x, x.y);
+            p[i + 1] = pack16<FP8>(y.x, y.y);
           }
-          l += s0 + s1;
+          l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
           tmem_st32(ta, p);
           tmem_wait_st();
         }
