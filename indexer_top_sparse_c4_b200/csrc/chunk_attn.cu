@@ -333,11 +333,16 @@ cudaError_t launch_simt_kv(const ChunkArgs& a, const ChunkWs& ws, int grid, floa
 }
 // Query rows of a tile of the few-rows kernel (8 or 16), or 0: the wide tiles
 // serve better.  The host knows the batch's tokens, not each request's.
+// Measured, 8 requests of 65,000 tokens, 16/2 heads, few against wide: 8 rows
+// (one token) D 256 BF16 166 : 216 us, FP8 107 : 213, D 128 BF16 93 : 170, FP8
+// 82 : 186; 16 rows D 128 97 : 169 and 97 : 186, but D 256 252 : 217 and 209 :
+// 218 (two columns of fragments leave too few registers there); 24 rows, two
+// passes over the cache, D 128 174 : 169 and D 256 475 : 218.
 int few_rows(const ChunkArgs& a) {
   const int G = a.Hq / a.Hkv;
   const int rows = (a.T + a.B - 1) / a.B * G;   // of an average request
   if (rows <= 8) return 8;
-  return rows <= 16 ? 16 : 0;
+  return rows <= 16 && a.D <= 128 ? 16 : 0;
 }
 
 template <int D>

@@ -51,10 +51,13 @@ struct FewCfg {
   static constexpr int RB = D * E < 128 ? D * E : 128;   // bytes of a box row
   static constexpr int kBoxes = D * E / RB;
   static constexpr int kSlot = kStep * D * E;            // a step's keys, or its values
-  // up to 160 KB of rings, three times what 6.5 TB/s keep in flight (128 KB
-  // beside the largest merge buffer)
-  static constexpr int W = kSlot >= 8192 ? 4 : 8;
-  static constexpr int kRing = (NT == 2 && W == 8 && D == 256 ? 128 : 160) * 1024;
+  // Warps: four for BF16 at D 256 (six: 176 instead of 167 us for 8 x 65,000
+  // tokens); twelve where a step's codes are few and its fixed part weighs
+  // (FP8 at D 128: 69 us, eight 81); else eight (twelve at D 256 FP8 are 3%
+  // faster at 262,144 tokens, 7% slower at 3,000).  Up to 160 KB of rings,
+  // three times what 6.5 TB/s keep in flight.
+  static constexpr int W = kSlot >= 8192 ? 4 : FP8 && D <= 128 && NT == 1 ? 12 : 8;
+  static constexpr int kRing = 160 * 1024;
   static constexpr int S = kRing / (W * kSlot) < 8 ? kRing / (W * kSlot) : 8;
 };
 
@@ -550,7 +553,10 @@ cudaError_t launch(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk, fl
 }
 template <int D, bool FP8>
 cudaError_t launch_nt(const ChunkArgs& a, const ChunkWs& ws, int rows, int grid, float qk, float vmul, cudaStream_t s) {
-  return rows == 8 ? launch<D, FP8, 1>(a, ws, grid, qk, vmul, s) : launch<D, FP8, 2>(a, ws, grid, qk, vmul, s);
+  if constexpr (D <= 128) {
+    if (rows == 16) return launch<D, FP8, 2>(a, ws, grid, qk, vmul, s);
+  }
+  return launch<D, FP8, 1>(a, ws, grid, qk, vmul, s);
 }
 template <int D>
 cudaError_t launch_kv(const ChunkArgs& a, const ChunkWs& ws, int rows, int grid, float qk, float vmul, cudaStream_t s) {
@@ -560,7 +566,7 @@ cudaError_t launch_kv(const ChunkArgs& a, const ChunkWs& ws, int rows, int grid,
 
 }  // namespace
 
-// rows: query rows of a tile, 8 or 16
+// rows: query rows of a tile, 8 or (D up to 128) 16
 cudaError_t launch_chunk_attn_few(const ChunkArgs& a, const ChunkWs& ws, int rows, int grid, float qk, float vmul,
                                   cudaStream_t s) {
   switch (a.D) {
