@@ -127,3 +127,17 @@ def test_binding_refuses_what_the_library_cannot_see():
         attn(lse=torch.zeros(5, 3))
     with pytest.raises(ValueError, match="shapes"):
         attn(cu_new=i(2))
+
+
+def test_binding_refuses_tensors_in_host_memory():
+    """A kernel must never be given a host address."""
+    from indexer_top_sparse_c4_b200 import qsa
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    z = torch.zeros
+    with pytest.raises(ValueError, match="CUDA"):
+        qsa.qsa_chunk_plan(i(2), i(2), i(4), i(2, 4), 8, i(3), i(2), i(5), i(5), i(5), i(1))
+    with pytest.raises(ValueError, match="CUDA"):
+        qsa.qsa_rope_write(z(5, 4, 64), z(5, 2, 64), z(5, 2, 64), i(5), z(32), i(5), z(5, 4, 64), z(2, 64, 2, 64),
+                           z(2, 64, 2, 64))
+    with pytest.raises(ValueError, match="CUDA"):
+        qsa.qsa_chunk_attn(z(5, 4, 64), z(2, 64, 2, 64), z(2, 64, 2, 64), i(2, 4), i(3), i(2), z(5, 4, 64))

@@ -365,3 +365,71 @@ def test_drafts_captured_and_repeated(q, q_dt, kv_dt):
         b.check()
         if kv[0] == 5001:
             assert torch.equal(first, b.out) and torch.equal(flse, b.lse)
+
+
+# ---- wide tiles: several items a worker, whole tiles, long rows in many parts -------
+
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS[:2])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_more_tiles_than_are_split(q, D, q_dt, kv_dt):
+    """Four tiles a worker and more: every tile is one worker's, in rounds."""
+    _run(q, [(i % 70, 17) for i in range(170)], 16, 1, D, q_dt, kv_dt, seed=30 + D, pad=1)
+
+
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS[:2])
+def test_more_tiles_than_the_table_holds(q, q_dt, kv_dt):
+    _run(q, [(i % 9, 17) for i in range(530)], 16, 1, 64, q_dt, kv_dt, seed=31)
+    _run(q, [(40, 1000)] + [(i % 130, 1) for i in range(1000)], 4, 1, 64, q_dt, kv_dt, seed=32)
+
+
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS[:2])
+@pytest.mark.parametrize("Hq, Hkv, D", [(16, 2, 256), (12, 1, 128), (8, 8, 64)])
+def test_wide_tiles_over_long_rows(q, Hq, Hkv, D, q_dt, kv_dt):
+    """A tile that every worker has a part of, beside short ones."""
+    _run(q, [(30011, 33)], Hq, Hkv, D, q_dt, kv_dt, seed=33)
+    _run(q, [(7000, 40), (3, 19), (129, 64), (0, 1), (4000, 21)], Hq, Hkv, D, q_dt, kv_dt, seed=34, pad=4)
+
+
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS[:2])
+def test_hidden_values_over_several_items(q, q_dt, kv_dt):
+    """Non-finite values in the last pages of some requests, in either half of a
+    head: each reaches the rows at and behind it, no other item."""
+    lens = [(100 + 7 * i, 24) for i in range(160)]
+    b = Batch(lens, 16, 2, 128, q_dt, kv_dt, seed=35)
+    for r, d, back in ((3, 5, 4), (3, 100, 1), (50, 127, 20), (159, 64, 24)):
+        p = int(b.kv_len[r]) - back
+        page, row = int(b.table[r, p // 64]), p % 64
+        if kv_dt == "fp8":
+            b.v.view(torch.uint8)[page, row, r % 2, d] = 0xff
+        else:
+            b.v[page, row, r % 2, d] = math.inf if r % 2 else math.nan
+    b.run(q)
+    b.check()
+    odd = (~torch.isfinite(b.out.float())).any(-1).any(-1).nonzero().flatten().tolist()
+    want = [24 * r + 24 - back + i for r, back in ((3, 4), (50, 20), (159, 24)) for i in range(back)]
+    assert odd == sorted(want)
+
+
+@pytest.mark.parametrize("kv_dt", ["bf16", "fp8"])
+def test_two_graphs_in_turn(q, kv_dt):
+    """Two captured calls of different shapes, each with its workspace, replayed
+    in turn on one stream."""
+    a = Batch([(2000, 1), (90, 1)], 16, 2, 256, "bf16", kv_dt, seed=36)
+    c = Batch([(500, 70), (0, 33)], 16, 2, 256, "bf16", kv_dt, seed=37)
+    graphs = []
+    for b in (a, c):
+        ws = b.workspace(q)
+        b.run(q, workspace=ws)
+        torch.cuda.synchronize()
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+            b.run(q, workspace=ws)
+        b.out.fill_(7.0)
+        b.lse.fill_(7.0)
+        graphs.append((g, ws))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, _ws in graphs:
+            g.replay()
+    a.check()
+    c.check()

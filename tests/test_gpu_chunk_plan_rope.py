@@ -156,7 +156,7 @@ def test_rope_types_and_pairs(q, D, rot, Hq, Hkv, adj, x, kv):
 @pytest.mark.parametrize("axes, inter", [(1, False), (1, True), (2, False), (2, True), (3, False), (3, True)])
 @pytest.mark.parametrize("T", [1, 3, 1184, 1185, 2501])
 def test_rope_axes_and_lengths(q, T, axes, inter):
-    """One token to many: one token and four tokens per CTA."""
+    """One token to many: parts of a token's heads and whole tokens to a warp."""
     _rope(q, T, 4, 2, 128, 96, axes=axes, inter=inter, seed=T)
 
 
