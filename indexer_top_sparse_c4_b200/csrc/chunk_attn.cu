@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
   pdl_wait();
   pdl_launch_dependents();
   if (tid == 0 && blockIdx.x < kChunkMaxCtas) ws.desc[blockIdx.x].n_parts = 0;
-  chunk_sched_build(a, sm.sched, TPT, kKeys, blockIdx.x, gridDim.x, false, 1);
+  chunk_sched_build(a, sm.sched, TPT, kKeys, blockIdx.x, gridDim.x, false, 2);
   ChunkWalk walk;
   walk.begin(a, sm.sched, blockIdx.x, gridDim.x);
   const QT* q = reinterpret_cast<const QT*>(a.q);

@@ -509,29 +509,32 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if constexpr (FP8) {                           // to FP16 in place, each thread what it brought
-          for (int r0 = 0; r0 < rows; r0 += 4 * RP) {
-            uint4 v[4];
+          constexpr int NB = 4;                        // rows at a time
+          for (int r0 = lt / CH; r0 < rows + lt / CH; r0 += NB * RP) {
+            uint4 v[NB];
+            __nv_bfloat162 top[NB];                    // the row's largest magnitude, of odd and even columns
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = r0 + k * RP + lt / CH;
+            for (int k = 0; k < NB; ++k) {
+              const int r = r0 + k * RP;
               v[k] = r < rows ? *at(r) : make_uint4(0, 0, 0, 0);
+              const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v[k]);
+              top[k] = __hmax2(__hmax2(__habs2(x[0]), __habs2(x[1])), __hmax2(__habs2(x[2]), __habs2(x[3])));
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = r0 + k * RP + lt / CH;
-              uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-              uint32_t top = 0;                        // the row's largest exponent field
+            for (int x = 1; x < CH; x <<= 1)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) top = max(top, max((w[e] >> 7) & 0xffu, (w[e] >> 23) & 0xffu));
+              for (int k = 0; k < NB; ++k) top[k] = __hmax2(top[k], __shfl_xor_sync(0xffffffffu, top[k], x));
 #pragma unroll
-              for (int x = 1; x < CH; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-              const uint32_t E = min(max(top, 11u), 254u);
+            for (int k = 0; k < NB; ++k) {
+              const int r = r0 + k * RP;
+              const uint32_t t = *reinterpret_cast<const uint32_t*>(&top[k]);
+              const uint32_t E = min(max(max((t >> 7) & 0xffu, (t >> 23) & 0xffu), 11u), 254u);
               const float up = __uint_as_float((264u - E) << 23);    // 2^(137 - E): the largest lands in 2^10 .. 2^11
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack16<true>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
+              auto to16 = [&](uint32_t w) {
+                return pack16<true>(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+              };
               if (r < rows) {
-                *at(r) = make_uint4(w[0], w[1], w[2], w[3]);
+                *at(r) = make_uint4(to16(v[k].x), to16(v[k].y), to16(v[k].z), to16(v[k].w));
                 if (c == 0) sm.q_scale[item & 1][r] = __uint_as_float((E - 10u) << 23);  // 2^(E - 137)
               }
             }
