@@ -53,8 +53,8 @@ struct FewCfg {
   static constexpr int kSlot = kStep * D * E;            // a step's keys, or its values
   // Warps: four for BF16 at D 256 (six: 176 instead of 167 us for 8 x 65,000
   // tokens); twelve where a step's codes are few and its fixed part weighs
-  // (FP8 at D 128: 69 us, eight 81); else eight (twelve at D 256 FP8 are 3%
-  // faster at 262,144 tokens, 7% slower at 3,000).  Up to 160 KB of rings,
+  // (FP8 at D 128: 69 us, eight 81); else eight (twelve at D 256 FP8 are 2%
+  // faster at 262,144 tokens, 9% slower at 3,000).  Up to 160 KB of rings,
   // three times what 6.5 TB/s keep in flight.
   static constexpr int W = kSlot >= 8192 ? 4 : FP8 && D <= 128 && NT == 1 ? 12 : 8;
   static constexpr int kRing = 160 * 1024;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
   int ls = 0, lns = 0, lwin = -1, lpage = 0, ly = 0;
   uint32_t issued = 0, badmask = 0;   // slots armed; by slot: a bad page
   uint32_t islot = 0;
-  bool lk = true, more = true;
+  bool lk = true, more = true, dead = false;       // dead: a wait has given up
   auto next_piece = [&]() {
     do {
       more = lwalk.next(a, sm.sched, TPT, KT, lit);
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
     } while (ls >= lns);
   };
   auto issue = [&]() {
-    if (!more || __any_sync(0xffffffffu, *abort_flag)) return;
+    if (!more || dead) return;
     if (lk) {
       const int lp = lit.blk_lo + ls / (KT / kStep);
       if (lwin < 0 || lp - lwin >= 32) {
@@ -226,22 +226,27 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
   ChunkItem it;
   uint32_t slot = 0, phase = 0, parity = 0;
   auto wait_slot = [&]() {
-    bool ok = !*abort_flag && mbar_wait(&sm.full[warp][slot], phase, abort_flag, a.status);
-    __syncwarp();
-    return ok;
+    // FP8: one look first, as reading the clock for a bounded wait costs more
+    // than most waits (8 x 262,144 tokens at D 256: 325 us, 365 without).  BF16
+    // waits for memory nearly always, and the look makes it slower (8 x 65,000
+    // tokens at D 256: 177 us, 169 without).
+    if (FP8 && __all_sync(0xffffffffu, mbar_test(&sm.full[warp][slot], phase))) return;
+    dead = dead || !__all_sync(0xffffffffu, !*abort_flag && mbar_wait(&sm.full[warp][slot], phase, abort_flag, a.status));
   };
   auto release = [&]() {
     __syncwarp();
     if (++slot == S) slot = 0, phase ^= 1;
     issue();
   };
-  // this lane's row address in a fragment load: matrices (keys 0-7, 8-15) x (chunk, chunk + 1)
+  // This lane's row in a fragment load: matrices (keys 0-7, 8-15) x (chunk,
+  // chunk + 1), chunk even.  Chunk c of key k lies at c ^ swizzle(k) of its
+  // row, so a lane's addresses differ by an exclusive or and the box.
   const int fkey = (lane & 7) + ((lane >> 3) & 1) * 8;
   const int fsw = C::RB == 128 ? fkey & 7 : (fkey >> 1) & 3;
-  auto frag_addr = [&](uint32_t base, int chunk) {   // chunk: even
-    const int ch = chunk + (lane >> 4);
+  const uint32_t flane = fkey * C::RB + (((lane >> 4) ^ fsw) << 4);
+  auto frag_addr = [&](uint32_t base, int chunk) {
     constexpr int CPB = C::RB / 16;
-    return base + (ch / CPB) * (kStep * C::RB) + fkey * C::RB + (((ch % CPB) ^ fsw) << 4);
+    return ((base + flane) ^ ((chunk % CPB) << 4)) + (chunk / CPB) * (kStep * C::RB);
   };
 
   while (walk.next(a, sm.sched, TPT, KT, it)) {

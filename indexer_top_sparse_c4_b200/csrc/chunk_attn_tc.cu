@@ -239,16 +239,6 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return r;
 }
 
-// One look at a phase.
-__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(saddr(b)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // A bounded wait that gives up at once when the CTA is stopping.  The first
 // look is the cheap one: a wait with a time limit costs some 200 cycles more.
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
