@@ -498,6 +498,10 @@ QSA_API qsa_status_t qsa_rope_write(const void* q, int q_stride, const void* k, 
  * cache runs on the tensor cores: logits, softmax and sums in FP32, the
  * probabilities rounded to the type of the product with V (BF16 for a BF16
  * cache, FP16 for an FP8 cache).  Other pairs run in FP32.
+ * The host sees the lengths' sum alone: T / B sets the height of the tiles, so
+ * a T far above the tokens in use (heavy padding) or one long chunk among many
+ * single tokens costs time, and another T may change results within those
+ * roundings.
  * Device checks: cu_new decreasing or outside [0, T], kv_len negative or past
  * the page table's row: QSA_DEV_ROW_RANGE (tokens past the row are not
  * attended); a page outside [0, num_pages): QSA_DEV_BAD_PAGE, its tokens are

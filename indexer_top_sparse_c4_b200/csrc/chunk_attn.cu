@@ -7,17 +7,19 @@
 //   out = sum_{j <= p} softmax(scale q . k_j) v_j,   lse = log sum_{j <= p} exp(scale q . k_j)
 //
 // This file holds the general kernel (every dtype pair, FP32 arithmetic on the
-// CUDA cores), the combine kernel that merges tiles several CTAs share, and
-// the choice between the general and the tensor-core kernel.
+// CUDA cores), the combine kernel that merges tiles several workers share, and
+// the choice between the general kernel and those on the tensor cores.
 //
 // General kernel: a CTA takes a tile of 32 query rows (whole tokens: all query
 // heads of one KV head) against one page of 64 keys at a time.  256 threads
-// hold 2 x 4 logits each (128 of 4 x 4 share loads better, but leave a
-// scheduler one warp to hide latencies with); the page's keys and values go through shared memory
+// hold 2 x 4 logits each; the page's keys and values go through shared memory
 // in FP32 and are read back as float4 (32 multiply-adds per 6 shared loads),
 // the running maximum and sum of the softmax stay in registers, 16 threads to
-// a row.  It is bound by the FP32 pipes and serves float32 models, whose
-// values the tensor cores would round.
+// a row.  It serves float32 models, whose values the tensor cores would round,
+// and is bound by the FP32 pipes for long prompts; a tiny model's (437 tokens,
+// 4/1 heads of D 64: 20 us) by the launch and one tile's latency.  128 threads
+// of 4 x 4 logits share loads better, but leave a scheduler one warp to hide
+// latencies with, and took as long.
 #include <math.h>
 
 #include "chunk_common.cuh"
