@@ -151,7 +151,10 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   FewSmem<D, FP8, NT>& sm =
       *reinterpret_cast<FewSmem<D, FP8, NT>*>(smem_raw + ((1024 - ((uintptr_t)smem_raw & 1023)) & 1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane >> 2, lc = lane & 3;
+  // the warp number by shuffle: the compiler then knows it, and what follows
+  // from it, as the same in all lanes
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31, lr = lane >> 2, lc = lane & 3;
   volatile int* abort_flag = &sm.abort_flag;
   const int G = a.Hq / a.Hkv, TPT = kRows / G;
   constexpr int KT = kPageTokens;
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
       ly = page < 0 ? -1 : page * kPageTokens + (ls % (KT / kStep)) * kStep;
     }
     badmask = (badmask & ~(1u << islot)) | ((ly < 0 ? 1u : 0u) << islot);
-    if (lane == 0) {
+    if (elect_one()) {
       mbar_arrive_tx(&sm.full[warp][islot], C::kSlot);
       const int y = ly < 0 ? a.num_pages * kPageTokens : ly;
 #pragma unroll
@@ -220,6 +223,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
         tma_load_3d(sm.ring[warp][islot] + b * (kStep * C::RB), lk ? &map_k : &map_v, &sm.full[warp][islot],
                     b * (C::RB / C::E), lit.kvh, y);
     }
+    __syncwarp();
     ++issued;
     if (++islot == S) islot = 0;
     lk = !lk;

@@ -257,16 +257,7 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile int*
   if (*abort_flag) return false;
   return mbar_wait(b, parity, abort_flag, status);
 }
-// One lane of a converged warp.  The compiler keeps the operands of MMAs issued
-// under it in uniform registers (16 MMAs take 153 cycles to issue); under a
-// comparison of the lane number it moves them there one by one (860 cycles,
-// more than the tensor cores need for a quarter of them).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-  return r != 0;
-}
-// The same by a whole warp, which is converged on return (the TMEM loads and
+// A wait by a whole warp, which is converged on return (the TMEM loads and
 // stores that follow need it).
 __device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
   return __all_sync(0xffffffffu, wait(b, parity, abort_flag, status));
