@@ -118,6 +118,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same onto zero
+template <bool F16>
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t widen(uint32_t codes) {  // two e4m3 codes (low 16 bits) to FP16
   uint32_t r;
   asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(r) : "r"(codes));
@@ -268,6 +283,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
     // Q as B operand: row n = lr + 8 nt
     uint32_t qf[NT][MT][2];
     float sc[NT][2], m[NT][2], l[NT][2];
+    float neg[NT][2], top[NT][2];                    // -m (0 while m is -infinity), and what a logit may reach
     int lim[NT][2];
     float o[NT][MT][4];
 #pragma unroll
@@ -313,6 +329,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
         sc[nt][j] = FP8 ? fmaxf(qk_scale_log2 * __shfl_sync(0xffffffffu, undo, (2 * lc + j) * 4), 1.2e-38f) : qk_scale_log2;
         lim[nt][j] = rr < rows ? min(it.p0 + rr / G + 1, it.kv) : it.kv;
         m[nt][j] = -INFINITY, l[nt][j] = 0.f;
+        neg[nt][j] = 0.f, top[nt][j] = -INFINITY;
       }
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -324,14 +341,8 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
       const int key0 = it.blk_lo * KT + s * kStep;
       const bool edge = key0 + kStep > lim0;
       // ---- S^T = K Q^T, CH chains of products each
-      constexpr int CH = 4 / NT;
+      constexpr int CH = 2;
       float sx[NT][CH][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sx[nt][c][j] = 0.f;
       wait_slot();
       const bool bad = (badmask >> slot) & 1;
       {
@@ -346,13 +357,17 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
               const uint32_t x = r[2 * h], y = r[2 * h + 1];
               const uint32_t a0 = widen(x), a1 = widen(y), a2 = widen(x >> 16), a3 = widen(y >> 16);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma16816<true>(sx[nt][(k + h) % CH], a0, a1, a2, a3, qf[nt][k + h][0], qf[nt][k + h][1]);
+              for (int nt = 0; nt < NT; ++nt) {
+                if (k + h < CH) mma16816_zero<true>(sx[nt][(k + h) % CH], a0, a1, a2, a3, qf[nt][k + h][0], qf[nt][k + h][1]);
+                else mma16816<true>(sx[nt][(k + h) % CH], a0, a1, a2, a3, qf[nt][k + h][0], qf[nt][k + h][1]);
+              }
             }
           } else {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816<false>(sx[nt][k % CH], r[0], r[1], r[2], r[3], qf[nt][k][0], qf[nt][k][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if (k < CH) mma16816_zero<false>(sx[nt][k % CH], r[0], r[1], r[2], r[3], qf[nt][k][0], qf[nt][k][1]);
+              else mma16816<false>(sx[nt][k % CH], r[0], r[1], r[2], r[3], qf[nt][k][0], qf[nt][k][1]);
+            }
           }
         }
       }
@@ -372,7 +387,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
             if (bad || key0 + lr + (j >> 1) * 8 >= lim[nt][j & 1]) x = -INFINITY;
           }
           sx[nt][0][j] = x;
-          grow = grow || x > m[nt][j & 1] + (kGrow + kShift) || (m[nt][j & 1] == -INFINITY && x > -INFINITY);
+          grow = grow || x > top[nt][j & 1];
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -387,6 +402,8 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
             const float alpha = m[nt][j] == mn ? 1.f : ex2(m[nt][j] - mn);
             m[nt][j] = mn;
             l[nt][j] *= alpha;
+            neg[nt][j] = mn == -INFINITY ? 0.f : -mn;
+            top[nt][j] = mn + (kGrow + kShift);
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[nt][i][j] *= alpha, o[nt][i][j + 2] *= alpha;
           }
@@ -396,7 +413,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
         float p[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          p[j] = ex2(sx[nt][0][j] - (m[nt][j & 1] == -INFINITY ? 0.f : m[nt][j & 1]));
+          p[j] = ex2(sx[nt][0][j] + neg[nt][j & 1]);
           l[nt][j & 1] += p[j];
         }
         pf[nt][0] = transpose8(pack16<FP8>(p[0], p[1]));
