@@ -13,12 +13,13 @@
 // widened copies and on rows that do not exist: 213 us where this kernel takes
 // 96 (8 x 65,000 tokens, 16/2 heads of D 256, FP8).
 //
-// Measured, 8 x 262,144 tokens, FP8: 325 us, 6.6 TB/s, the rate of a plain
-// copy.  Then what a warp issues counts as much as what memory gives: per SM
-// sub-partition a product takes 8 cycles, a conversion of two codes 2 (4 for
-// the upper two of a word), a byte permutation 2, and dropping a clock read
-// and two votes per step took the call from 365 us to 325.  BF16 at D 256 runs at 0.96
-// of the copy rate (8 x 65,000 tokens, 169 us).
+// Measured, 8 x 262,144 tokens, FP8: 316 us, 6.8 TB/s, 1.04 of what a plain copy
+// reaches.  What a warp issues counts as much as what memory gives: per SM
+// sub-partition a product takes 8 cycles, a conversion of two codes 2 (4 for the
+// upper two of a word), a byte permutation 2; a clock read and two votes less
+// per step took the call from 365 us to 325, and under the power limit, at 1.75
+// GHz, copies issued under elect.sync and shorter softmax steps from 375 to 342.
+// BF16 at D 256: 165 us for 8 x 65,000 tokens, 0.98 of the copy rate.
 //
 //  * every warp works on its own: it takes every W-th step of 16 keys of the
 //    CTA's piece, loads keys and values by TMA into its own ring (one lane
@@ -62,11 +63,14 @@ struct FewCfg {
   static constexpr int kSlot = kStep * D * E;            // a step's keys, or its values
   // Warps: four for BF16 at D 256 (six: 176 instead of 167 us for 8 x 65,000
   // tokens); twelve where a step's codes are few and its fixed part weighs
-  // (FP8 at D 128: 69 us, eight 81); else eight (twelve at D 256 FP8 are 2%
-  // faster at 262,144 tokens, 9% slower at 3,000).  Up to 160 KB of rings,
-  // three times what 6.5 TB/s keep in flight.
+  // (FP8 at D 128: 69 us, eight 81); else eight (twelve at D 256 FP8: 332 instead
+  // of 342 us for 8 x 262,144 tokens when power holds the clock down, but 48.4
+  // instead of 46.7 for 64 x 3,000).
   static constexpr int W = kSlot >= 8192 ? 4 : FP8 && D <= 128 && NT == 1 ? 12 : 8;
-  static constexpr int kRing = 160 * 1024;
+  // 96 KB of rings, twice what 6.5 TB/s keep in flight.  More is slower, as if
+  // memory served fewer streams better: 8 x 262,144 tokens FP8 316 us with 96
+  // KB, 330 with 128 or 160, 327 with 64; 8 x 65,000 BF16 165, 173, 180, 171.
+  static constexpr int kRing = 96 * 1024;
   static constexpr int S = kRing / (W * kSlot) < 8 ? kRing / (W * kSlot) : 8;
 };
 
@@ -254,10 +258,9 @@ __global__ void __launch_bounds__(FewCfg<D, FP8, NT>::W * 32, 1)
   ChunkItem it;
   uint32_t slot = 0, phase = 0, parity = 0;
   auto wait_slot = [&]() {
-    // FP8: one look first, as reading the clock for a bounded wait costs more
-    // than most waits (8 x 262,144 tokens at D 256: 325 us, 365 without).  BF16
-    // waits for memory nearly always, and the look makes it slower (8 x 65,000
-    // tokens at D 256: 177 us, 169 without).
+    // One look first: reading the clock for a bounded wait costs more than most
+    // waits of an FP8 cache (8 x 262,144 tokens at D 256: 325 us, 365 without).
+    // BF16 waits for memory nearly always.
     if (FP8 && __all_sync(0xffffffffu, mbar_test(&sm.full[warp][slot], phase))) return;
     dead = dead || !__all_sync(0xffffffffu, !*abort_flag && mbar_wait(&sm.full[warp][slot], phase, abort_flag, a.status));
   };
