@@ -334,17 +334,20 @@ cudaError_t launch_simt_kv(const ChunkArgs& a, const ChunkWs& ws, int grid, floa
   }
 }
 // Query rows of a tile of the few-rows kernel (8 or 16), or 0: the wide tiles
-// serve better.  The host knows the batch's tokens, not each request's.
-// Measured, 8 requests of 65,000 tokens, 16/2 heads, few against wide: 8 rows
-// (one token) D 256 BF16 166 : 216 us, FP8 107 : 213, D 128 BF16 93 : 170, FP8
-// 82 : 186; 16 rows D 128 97 : 169 and 97 : 186, but D 256 252 : 217 and 209 :
-// 218 (two columns of fragments leave too few registers there); 24 rows, two
-// passes over the cache, D 128 174 : 169 and D 256 475 : 218.
+// serve better.  The host knows the batch's tokens, not each request's.  Above
+// 16 rows the narrow tiles read the cache once per 16.
+// Measured, 16/2 heads, narrow against wide (us):
+//   rows  batch         D 256 BF16  FP8        D 128 BF16  FP8
+//   8     8 x 65,000    164 : 218   91 : 211   88 : 168    56 : 189
+//   16    8 x 65,000    175 : 219   118 : 212  92 : 169    78 : 189
+//   24    8 x 65,000    330 : 221   199 : 214  165 : 169   137 : 189
+//   32    8 x 65,000    331 : 206   201 : 199  167 : 141   137 : 155
+//   32    64 x 300      43 : 31     44 : 37    29 : 26     29 : 29
 int few_rows(const ChunkArgs& a) {
   const int G = a.Hq / a.Hkv;
   const int rows = (a.T + a.B - 1) / a.B * G;   // of an average request
-  if (rows <= 8) return 8;
-  return rows <= 16 && a.D <= 128 ? 16 : 0;
+  const int most = 16 + (a.kv_dt == QSA_FP8_E4M3 ? 8 : 0) + (a.D <= 128 ? 8 : 0);
+  return rows <= 8 ? 8 : rows <= most ? 16 : 0;
 }
 
 template <int D>

@@ -10,8 +10,8 @@
 // values go from shared memory through registers once, and FP8 codes are
 // widened there (e4m3 is a subset of FP16) without a second trip through
 // shared memory.  The wide tcgen05 tiles spend shared-memory traffic on
-// widened copies and on rows that do not exist: 213 us where this kernel takes
-// 96 (8 x 65,000 tokens, 16/2 heads of D 256, FP8).
+// widened copies and on rows that do not exist: 211 us where this kernel takes
+// 91 (8 x 65,000 tokens, 16/2 heads of D 256, FP8).
 //
 // Measured, 8 x 262,144 tokens, FP8: 316 us, 6.8 TB/s, 1.04 of what a plain copy
 // reaches.  What a warp issues counts as much as what memory gives: per SM
@@ -591,10 +591,7 @@ cudaError_t launch(const ChunkArgs& a, const ChunkWs& ws, int grid, float qk, fl
 }
 template <int D, bool FP8>
 cudaError_t launch_nt(const ChunkArgs& a, const ChunkWs& ws, int rows, int grid, float qk, float vmul, cudaStream_t s) {
-  if constexpr (D <= 128) {
-    if (rows == 16) return launch<D, FP8, 2>(a, ws, grid, qk, vmul, s);
-  }
-  return launch<D, FP8, 1>(a, ws, grid, qk, vmul, s);
+  return rows == 8 ? launch<D, FP8, 1>(a, ws, grid, qk, vmul, s) : launch<D, FP8, 2>(a, ws, grid, qk, vmul, s);
 }
 template <int D>
 cudaError_t launch_kv(const ChunkArgs& a, const ChunkWs& ws, int rows, int grid, float qk, float vmul, cudaStream_t s) {
@@ -604,7 +601,7 @@ cudaError_t launch_kv(const ChunkArgs& a, const ChunkWs& ws, int rows, int grid,
 
 }  // namespace
 
-// rows: query rows of a tile, 8 or (D up to 128) 16
+// rows: query rows of a tile, 8 or 16
 cudaError_t launch_chunk_attn_few(const ChunkArgs& a, const ChunkWs& ws, int rows, int grid, float qk, float vmul,
                                   cudaStream_t s) {
   switch (a.D) {
