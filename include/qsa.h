@@ -494,7 +494,7 @@ QSA_API qsa_status_t qsa_rope_write(const void* q, int q_stride, const void* k, 
  * they hold, and neither is a token in a row's result that the row does not
  * see (NaN or infinity included).
  * Supported: D 64, 128, 256; Hq/Hkv <= 16; q F32 or BF16; caches F32, BF16 or
- * FP8_E4M3 (value = code * scale); B <= 1,024.  A BF16 query on a BF16 or FP8
+ * FP8_E4M3 (value = code * scale); B <= 1,024; pt_stride <= 2^20.  A BF16 query on a BF16 or FP8
  * cache runs on the tensor cores: logits, softmax and sums in FP32, the
  * probabilities rounded to the type of the product with V (BF16 for a BF16
  * cache, FP16 for an FP8 cache).  Other pairs run in FP32.

@@ -39,6 +39,7 @@ constexpr int kMaxGridY = 65535;
 constexpr int kMaxChunkTokens = 1 << 20;   // tokens of a plan, rotary or chunk-attention call
 constexpr int kMaxPages = (1 << 25) - 1;    // token rows of a cache stay below 2^31
 constexpr int kMaxRowPages = 1 << 24;       // tokens of a page-table row stay well below 2^31
+constexpr int kMaxAttnPages = 1 << 20;      // the key blocks of 1,024 query tiles stay below 2^31
 constexpr int kPageGroupsAbi = 16;   // groups per 64-token page
 
 qsa_status_t check_attn(const void* q, qsa_dtype_t q_dt, const void* k_pages, const void* v_pages,
@@ -589,7 +590,7 @@ qsa_status_t qsa_chunk_attn(const void* q, qsa_dtype_t q_dt, const void* k_pages
   SUPPORT((long long)Hq * D <= (1 << 24), "too many heads (Hq=%d)", Hq);
   REQUIRE(num_pages >= 1 && pt_rows >= 1 && pt_stride >= 1, "num_pages, pt_rows and pt_stride must be >= 1");
   SUPPORT(num_pages <= kMaxPages, "num_pages = %d exceeds %d", num_pages, kMaxPages);
-  SUPPORT(pt_stride <= kMaxRowPages, "pt_stride = %d exceeds %d", pt_stride, kMaxRowPages);
+  SUPPORT(pt_stride <= kMaxAttnPages, "pt_stride = %d exceeds %d", pt_stride, kMaxAttnPages);
   REQUIRE(B <= pt_rows, "B = %d requests need as many page-table rows (got %d)", B, pt_rows);
   REQUIRE(q_dt == QSA_F32 || q_dt == QSA_BF16, "q dtype must be F32 or BF16");
   REQUIRE(kv_dt == QSA_F32 || kv_dt == QSA_BF16 || kv_dt == QSA_FP8_E4M3, "bad KV dtype");

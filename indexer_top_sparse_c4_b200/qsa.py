@@ -553,7 +553,7 @@ def qsa_chunk_plan(n_cached, n_new, free_pages, page_table, num_pages, cu_new, k
     old, new, free, table, *out = _pointers(dev, n_cached, n_new, free_pages, page_table, cu_new, kv_len, q_req, q_pos,
                                             slot, n_taken, dev_status)
     _call(lib().qsa_chunk_plan, dev, stream, old, new, B, free, free_pages.numel(), table, shape[0], shape[1],
-          num_pages, T, *out)
+          int(num_pages), T, *out)
     return cu_new, kv_len, q_req, q_pos, slot, n_taken
 
 
@@ -589,7 +589,7 @@ def qsa_rope_write(q, k, v, pos, inv_freq, slot, q_out, k_pages, v_pages, sectio
     axes = 1 if len(ps) == 1 else ps[0]
     if axes > 1 and sections is None:
         raise ValueError("several axes need their sections")
-    sec = (half, 0, 0) if sections is None else (*sections, *(0,) * (3 - len(sections)))
+    sec = (half, 0, 0) if sections is None else (*map(int, sections), *(0,) * (3 - len(sections)))
     if len(sec) != 3 or not 1 <= axes <= 3:
         raise ValueError("one to three axes and sections")
     _int32("pos and slot", pos, slot)
@@ -615,7 +615,8 @@ def qsa_rope_write(q, k, v, pos, inv_freq, slot, q_out, k_pages, v_pages, sectio
     freq_p, slot_p, out_p, k_p, v_p, st_p = _pointers(dev, inv_freq, slot, q_out, k_pages, v_pages, dev_status)
     _call(lib().qsa_rope_write, dev, stream, qp, qs, kp, ks, vp, vs, x_dt, pos.data_ptr(), axes,
           pos.stride(0) if axes > 1 else T, *sec, 1 if interleaved_axes else 0, 1 if adjacent_pairs else 0, freq_p,
-          2 * half, rot_scale, slot_p, T, Hq, Hkv, D, out_p, k_p, v_p, kv_dt, k_scale, v_scale, num_pages, st_p)
+          2 * half, float(rot_scale), slot_p, T, Hq, Hkv, D, out_p, k_p, v_p, kv_dt, float(k_scale), float(v_scale),
+          num_pages, st_p)
     return q_out
 
 
@@ -649,7 +650,7 @@ def qsa_chunk_attn(q, k_pages, v_pages, page_table, cu_new, kv_len, out, workspa
     q_p, k_p, v_p, pt_p, cu_p, kv_p, out_p, lse_p, ws_p, st_p = _pointers(
         dev, q, k_pages, v_pages, page_table, cu_new, kv_len, out, lse, workspace, dev_status)
     rows, width = page_table.shape
-    _call(lib().qsa_chunk_attn, dev, stream, q_p, q_dt, k_p, v_p, kv_dt, k_scale, v_scale, num_pages, pt_p, rows, width,
-          cu_p, kv_p, B, T, Hq, Hkv, D, sm_scale, out_p, lse_p, ws_p,
+    _call(lib().qsa_chunk_attn, dev, stream, q_p, q_dt, k_p, v_p, kv_dt, float(k_scale), float(v_scale), num_pages, pt_p,
+          rows, width, cu_p, kv_p, B, T, Hq, Hkv, D, float(sm_scale), out_p, lse_p, ws_p,
           0 if workspace is None else workspace.numel() * workspace.element_size(), st_p)
     return out

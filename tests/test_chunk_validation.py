@@ -72,6 +72,7 @@ def _attn(L, T=4, B=2, Hq=16, Hkv=2, D=256, q_dt=1, kv_dt=1, ptr=OK, q=OK, pt_ro
     (dict(Hq=17, Hkv=1), 2, "16 query heads"), (dict(D=96), 2, "head dim"), (dict(B=3), 1, "page-table rows"),
     (dict(num_pages=1 << 25), 2, "num_pages"), (dict(pt_stride=0), 1, "pt_stride"),
     (dict(pt_stride=(1 << 24) + 1), 2, "pt_stride"), (dict(q_dt=2), 1, "q dtype"), (dict(kv_dt=5), 1, "KV dtype"),
+    (dict(pt_stride=(1 << 20) + 1), 2, "pt_stride"),
     (dict(kv_dt=2, scale=-1.0), 1, "FP8"), (dict(sm=float("nan")), 1, "sm_scale"), (dict(ptr=NULL), 1, "null"),
     (dict(q=ODD), 1, "aligned"), (dict(ws=NULL), 3, "workspace"), (dict(ws_bytes=1024), 3, "workspace"),
     (dict(ws=ODD), 3, "workspace"),

@@ -156,3 +156,31 @@ def test_a_captured_step_serves_every_batch(q, kv):
         g.replay()
     for news in ([60, 1, 30, 64], [1, 1, 1, 1], [2, 100, 3, 1], [1, 0, 1, 1], [0, 0, 0, 0], [4, 4, 4, 4]):
         loop.step(news, run=run)
+
+
+def test_bound_calls(q):
+    """The rotary and attention calls bound once, called again on refilled
+    buffers; scales and sections as numpy and torch scalars."""
+    import numpy as np
+    b = cu_.Batch([(200, 2), (0, 33)], 8, 2, 128, "bf16", "fp8", seed=7)
+    ws = b.workspace(q)
+    b.k_scale, b.v_scale = np.float32(b.k_scale), torch.tensor(b.v_scale)
+    go = q.bind(b.run, q, workspace=ws)
+    torch.cuda.synchronize()
+    assert bool((b.out == 7).all())          # binding ran nothing
+    b.k_scale, b.v_scale = float(b.k_scale), float(b.v_scale)
+    for _ in range(2):
+        b.q.copy_(torch.randn(b.q.shape, device="cuda"))
+        go()
+        b.check()
+    x = torch.zeros((3, 4, 64), device="cuda")
+    kc, vc = (torch.zeros((1, 64, 4, 64), device="cuda") for _ in range(2))
+    pos = torch.zeros((3, 3), dtype=torch.int32, device="cuda")
+    slot = torch.arange(3, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(x)
+    go = q.bind(q.qsa_rope_write, x, x, x, pos, torch.ones(32, device="cuda"), slot, out, kc, vc,
+                sections=np.array([12, 10, 10]), rot_scale=np.float64(2.0))
+    x.fill_(3.0)
+    go()
+    torch.cuda.synchronize()
+    assert bool((out == 6).all()) and bool((kc.view(-1, 4, 64)[:3] == 6).all()) and bool((vc.view(-1, 4, 64)[:3] == 3).all())
