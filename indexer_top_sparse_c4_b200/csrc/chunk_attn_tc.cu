@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
   constexpr float kShift = FP8 ? 7.f : 0.f;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   TcSmem<D, FP8>& sm = *reinterpret_cast<TcSmem<D, FP8>*>(smem_raw + ((1024 - ((uintptr_t)smem_raw & 1023)) & 1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: uniform
   volatile int* abort_flag = &sm.abort_flag;
   const int G = a.Hq / a.Hkv, TPT = 2 * kRows / G;
   const uint32_t rank = cluster_rank();
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
           const int y0 = __shfl_sync(0xffffffffu, from, x & 31), y1 = __shfl_sync(0xffffffffu, from, (x + 1) & 31);
           ok = wait_warp(&empties[s], phase ^ 1, abort_flag, a.status);
           if (!ok) return;
-          if (lane == 0) {
+          if (elect_one()) {
             uint64_t* const own = &sm.raw_full[FP8 ? s : 0];
             const uint32_t bar = map_cta(saddr(&sm.full[FP8 ? 0 : s]), 0);
             unsigned char* dst = FP8 ? sm.raw[s] : sm.stage[s];
