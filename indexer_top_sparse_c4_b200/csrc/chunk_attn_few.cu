@@ -34,7 +34,8 @@
 //    consecutive dimensions that a thread's 32-bit word holds.
 //  * the softmax reference moves (and O^T is rescaled) only when a logit has
 //    outgrown it by 2^8; for an FP8 cache P is kept 2^7 larger, so that small
-//    probabilities stay in FP16's normal range down to 2^-21 of the largest.
+//    probabilities stay in FP16's normal range down to 2^-21 of the largest
+//    (smaller ones are rounded by 2^-32 of the largest).
 //  * the warps' results are merged in shared memory at the end of a piece, the
 //    pieces of a tile by the combine kernel, both in a fixed order.
 //  * FP8 queries: see the power-of-two row scale of chunk_attn_tc.cu.
