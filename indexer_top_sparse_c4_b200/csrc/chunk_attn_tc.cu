@@ -33,7 +33,7 @@
 //    4..11 do the softmax of the CTA's rows (two warps per TMEM lane quarter,
 //    64 keys each), and warps 2 and 3 bring the next item's queries by cp.async.
 //  * FP8 cache: boxes of codes land in a second ring, and warps 12..15 turn
-//    them into FP16 slots (e4m3 is a subset of FP16, the product P V then
+//    them into FP16 stages (e4m3 is a subset of FP16, the product P V then
 //    takes P in FP16).  The query is FP16 too: each row is scaled by a power
 //    of two that puts its largest value at 2^10 .. 2^11, which keeps all bits
 //    of every BF16 value down to 2^-24 of the row's largest; the scale is
@@ -41,7 +41,7 @@
 //  * tiles that hold keys some row must not see ("edge" tiles: the causal
 //    diagonal, the last page): masked P is 0, but 0 x NaN is NaN in the matrix
 //    product, so the softmax warps first clear the value rows past the last
-//    token and any non-finite value of the tile from its V slots.  Non-finite
+//    token and any non-finite value of the tile from its V stage.  Non-finite
 //    values that a row does see are added back to its output at the end (the
 //    `poison` flag; the sum is then non-finite whatever its weight).
 //  * few tiles: the (tile, key block) space is divided evenly over the pairs and

@@ -1,13 +1,13 @@
 // chunk_common.cuh -- what the kernels of the chunk attention share: the
 // reading of a request's lengths, the cut of the work into tiles of query rows
-// and blocks of keys, and each CTA's share of it.
+// and blocks of keys, and the share of it of each worker (a CTA, or a pair).
 #pragma once
 #include "umma.cuh"
 
 namespace qsa {
 
 constexpr int kChunkMaxReq = 1024;   // requests per chunk-attention call
-constexpr int kChunkMaxTiles = 1024; // query tiles per KV head of a call whose tiles are split over CTAs
+constexpr int kChunkMaxTiles = 1024; // query tiles per KV head of a call whose tiles are split over workers
 constexpr int kChunkMaxCtas = 148;   // CTAs that leave partials (one per SM of a B200; half as many pairs)
 
 // A request as the device arrays give it.  `kv` is capped to the tokens a row
@@ -25,7 +25,7 @@ __device__ __forceinline__ ChunkReq chunk_req(const ChunkArgs& a, int b, bool re
   return ChunkReq{lo, hi - lo, kv - (hi - lo), min(kv, cap)};
 }
 
-// One CTA's piece of work: key blocks [blk_lo, blk_hi) of a tile of query
+// One worker's piece of work: key blocks [blk_lo, blk_hi) of a tile of query
 // tokens and one KV head.
 struct ChunkItem {
   int b, kvh, t0, ntok, p0, kv;
@@ -34,10 +34,10 @@ struct ChunkItem {
   int n_parts;   // > 0: this piece holds the tile's first block, and so many pieces share the tile
 };
 
-// What a combine CTA needs to know of a tile that several CTAs share; entry c
-// is written by CTA c (n_parts = 0: none of CTA c's pieces opens a shared tile).
-// Partial slots: 2c + 1 for a piece that opens a tile CTA c does not finish,
-// 2c for a piece that starts inside a tile (CTA c's first).
+// What a combine CTA needs to know of a tile that several workers share; entry
+// c is written by worker c (n_parts = 0: none of its pieces opens a shared
+// tile).  Partial slots: 2c + 1 for a piece that opens a tile worker c does not
+// finish, 2c for a piece that starts inside a tile (its first).
 struct ChunkDesc {
   int n_parts, t0, ntok, kvh;
 };
@@ -48,8 +48,8 @@ struct ChunkDesc {
 // workers, whatever the requests' lengths, and tiles that several share are
 // merged by the combine kernel.  A tile's units are its key blocks behind a
 // lead: what its start and end cost, in blocks, so that a worker with many
-// short tiles does not finish last.  With many tiles (four per CTA, or more
-// than the table holds) every tile is one CTA's; neighbouring CTAs then walk
+// short tiles does not finish last.  With many tiles (four per worker, or
+// more than the table holds) every tile is one worker's; neighbours then walk
 // the same keys at about the same time and share them in L2, and rounds run
 // in alternating order so that the causal tiles' growing lengths even out.
 struct ChunkSched {
