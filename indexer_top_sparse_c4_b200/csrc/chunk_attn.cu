@@ -17,7 +17,7 @@
 // the running maximum and sum of the softmax stay in registers, 16 threads to
 // a row.  It serves float32 models, whose values the tensor cores would round,
 // and is bound by the FP32 pipes for long prompts; a tiny model's (437 tokens,
-// 4/1 heads of D 64: 20 us) by the launch and one tile's latency.  128 threads
+// 4/1 heads of D 64: 18 us) by the launch and one tile's latency.  128 threads
 // of 4 x 4 logits share loads better, but leave a scheduler one warp to hide
 // latencies with, and took as long.
 #include <math.h>
@@ -222,7 +222,10 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
 // by itself.  More (long decode rows): a row's partials are spread over the 8
 // warps and joined in shared memory.  The order of the sums is fixed.
 constexpr int kCombineThreads = 256;
-constexpr int kCombineY = 16;
+// CTAs to a worker's tile.  Narrow tiles: 8, as most of a small step's only find
+// that nothing is shared (one request of 64 tokens: 9.5 us, 10.7 with 16); else
+// 16 (8: float32 prompts 23 us instead of 20).
+constexpr int kCombineFew = 8, kCombineWide = 16;
 template <int D, typename OT>
 __global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(ChunkArgs a, ChunkWs ws, int tile_rows,
                                                                         float vmul) {
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(ChunkArg
   const int G = a.Hq / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int first = 2 * blockIdx.x + 1;                 // then 2 (blockIdx.x + i), i = 1 .. n_parts - 1
   if (dsc.n_parts <= W) {
-    for (int r = blockIdx.y * W + warp; r < dsc.ntok * G; r += kCombineY * W) {
+    for (int r = blockIdx.y * W + warp; r < dsc.ntok * G; r += gridDim.y * W) {
       // lane i: the maximum and sum of part i, and its weight
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < dsc.n_parts) ml = ws.ml[(size_t)(lane == 0 ? first : 2 * (blockIdx.x + lane)) * tile_rows + r];
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(ChunkArg
     }
     return;
   }
-  for (int r = blockIdx.y; r < dsc.ntok * G; r += kCombineY) {
+  for (int r = blockIdx.y; r < dsc.ntok * G; r += gridDim.y) {
     float m = -INFINITY, l = 0.f, o[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) o[j] = 0.f;
@@ -364,7 +367,7 @@ cudaError_t launch_d(const ChunkArgs& a, void* wsp, int grid, float qk, float vm
   if (e != cudaSuccess) return e;
   auto comb = a.q_dt == QSA_F32 ? chunk_combine_kernel<D, float> : chunk_combine_kernel<D, __nv_bfloat16>;
   const int workers = tc && !few ? grid / 2 : grid;   // who may have opened a tile that others finish
-  return launch_k(comb, dim3(workers, kCombineY), dim3(kCombineThreads), 0, s, 1, a, ws, rows, vmul);
+  return launch_k(comb, dim3(workers, few ? kCombineFew : kCombineWide), dim3(kCombineThreads), 0, s, 1, a, ws, rows, vmul);
 }
 
 }  // namespace
