@@ -680,9 +680,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       sm.lx[half][row] = l;
       bar_sync(5, 256);
       l += sm.lx[half ^ 1][row];
-      const bool poison = sm.poison[item & 3] != 0;
       wait_warp(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, a.status);
       tc_fence_after();
+      // The other CTA clears its half of V's columns and sets the flag here before
+      // it hands over the tile's P: the item's last product is what orders both
+      // with this read (bar_sync joins the warps of one CTA only).
+      const bool poison = *reinterpret_cast<volatile int*>(&sm.poison[item & 3]) != 0;
       if (warp_live) {
         const size_t orow = (size_t)(it.t0 + tok) * a.Hq + it.kvh * G + (trow - tok * G);
         const size_t prow_out = (size_t)max(it.part, 0) * (2 * kRows) + trow;
