@@ -110,7 +110,7 @@ struct TcSmem {
   uint64_t raw_full[C::kRaws ? C::kRaws : 1], raw_empty[C::kRaws ? C::kRaws : 1];
   uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free, v_ready, drain;
   float mx[2][2][kRows];                 // [tile parity][half][row] maxima
-  float lx[2][kRows];                    // [half][row] sums
+  float lx[2][2][kRows];                 // [item parity][half][row] sums
   float q_scale[2][kRows];               // FP8, by item parity: what undoes the row's power of two
   alignas(16) unsigned char out[kSoftWarps][32 * 64];   // 64 bytes of a warp's 32 output rows
   int poison[4];                         // by item, modulo 4
@@ -677,9 +677,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
       // The flag of the item after next: its last readers are past the barrier of
       // the item before this one, its writers behind the P of the next one.
       if (st == 0) sm.poison[(item + 2) & 3] = 0;
-      sm.lx[half][row] = l;
+      // By item parity: a warp without rows in the next item may be through with it
+      // before its partner has read this one's sum.
+      sm.lx[item & 1][half][row] = l;
       bar_sync(5, 256);
-      l += sm.lx[half ^ 1][row];
+      l += sm.lx[item & 1][half ^ 1][row];
       wait_warp(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, a.status);
       tc_fence_after();
       // The other CTA clears its half of V's columns and sets the flag here before

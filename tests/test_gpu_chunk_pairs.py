@@ -65,3 +65,22 @@ def test_nan_that_the_other_block_clears(q, q_dt, kv_dt, D, late):
     col = 5 if late == 0 else D - 3
     odd = torch.isnan(b.out[:, 0, col].float()).view(-1, 16)
     assert bool(odd[1, 15]) and not bool(odd[0].any()) and int(odd[1].sum()) == (1 if late == 0 else 12)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_dt, kv_dt", KINDS)
+def test_full_items_before_nearly_empty_ones(q, q_dt, kv_dt, D):
+    """16 tokens of 16 heads, every row of a tile, then a single token's long row,
+    whose pieces leave most warps without a row and end anywhere: warps with
+    nothing to do are an item ahead of the others."""
+    lens = [x for i in range(40) for x in ((300 + 13 * i, 16), (3000 + 211 * i, 1))]
+    b = Batch(lens, 16, 1, D, q_dt, kv_dt, seed=50)
+    ref, ws, first = with_fp16_tail(b, b.reference()), b.workspace(q), None
+    for _ in range(20):
+        b.out.fill_(7.0)
+        b.lse.fill_(7.0)
+        b.run(q, workspace=ws)
+        b.check(ref=ref)
+        got = b.out.clone().view(torch.int16)
+        assert first is None or torch.equal(first, got)
+        first = got
