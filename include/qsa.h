@@ -431,7 +431,8 @@ QSA_API qsa_status_t qsa_dcp_merge_attn(const float* o_parts, const float* lse_p
  * in batch order (request 0's pages first) and every other entry stays as it
  * is.  Rows of q_req, q_pos and slot behind the last token get -1 (a padded
  * batch).  The inputs are not changed: a caller drops the first n_taken pages
- * from its free list.
+ * from its free list.  B = 0 is an idle step: cu_new[0] and n_taken[0] are 0,
+ * the T rows get -1, and n_cached, n_new, kv_len and page_table may be NULL.
  * Device checks: a negative length counts as 0; tokens past T are cut (cu_new
  * and kv_len count the tokens kept); tokens past the page table's row have
  * slot -1 (all three: QSA_DEV_ROW_RANGE); when the free list runs out, the

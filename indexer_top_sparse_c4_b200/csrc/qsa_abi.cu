@@ -510,12 +510,14 @@ qsa_status_t qsa_chunk_plan(const int32_t* n_cached, const int32_t* n_new, int B
   REQUIRE(B >= 0 && T >= 0 && n_free >= 0, "B, T and n_free must be >= 0 (got %d, %d, %d)", B, T, n_free);
   SUPPORT(B <= qsa::chunk_plan_max_requests(), "B = %d exceeds %d requests per call", B, qsa::chunk_plan_max_requests());
   SUPPORT(T <= kMaxChunkTokens, "T = %d exceeds %d tokens per call", T, kMaxChunkTokens);
-  REQUIRE(num_pages >= 1 && pt_rows >= 1 && pt_stride >= 1, "num_pages, pt_rows and pt_stride must be >= 1");
+  REQUIRE(num_pages >= 1 && pt_rows >= (B > 0) && pt_stride >= 1, "num_pages, pt_rows and pt_stride must be >= 1");
   SUPPORT(num_pages <= kMaxPages, "num_pages = %d exceeds %d", num_pages, kMaxPages);
   SUPPORT(pt_stride <= kMaxRowPages, "pt_stride = %d exceeds %d", pt_stride, kMaxRowPages);
   REQUIRE(B <= pt_rows, "B = %d requests need as many page-table rows (got %d)", B, pt_rows);
-  if (B == 0 && T == 0) return QSA_OK;
-  REQUIRE(n_cached && n_new && page_table && cu_new && kv_len && n_taken, "null pointer argument");
+  // an idle step still says that it has no token and took no page
+  if (B == 0 && T == 0 && !cu_new && !n_taken) return QSA_OK;
+  REQUIRE(cu_new && n_taken, "null pointer argument");
+  REQUIRE(B == 0 || (n_cached && n_new && page_table && kv_len), "null pointer argument");
   REQUIRE(free_pages || n_free == 0, "free_pages is NULL with n_free = %d", n_free);
   REQUIRE(T == 0 || (q_req && q_pos && slot), "null pointer argument");
   qsa::PlanArgs a{n_cached, n_new, B, free_pages, n_free, page_table, pt_rows, pt_stride, num_pages, cu_new, kv_len,
