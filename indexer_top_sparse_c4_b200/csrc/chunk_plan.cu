@@ -71,10 +71,10 @@ __device__ __forceinline__ long long scan(long long v, long long* warp_sum, long
 }
 
 __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(PlanArgs a) {
-  extern __shared__ int smem[];
-  int* cu = smem;               // [B + 1] tokens before each request, cut at T
-  int* base = smem + a.B + 1;   // [B + 1] free pages taken before each request
-  __shared__ long long warp_sum[kThreads / 32];
+  extern __shared__ long long smem[];             // all of the kernel's: plan_smem below counts it
+  long long* warp_sum = smem;                     // [kThreads / 32]
+  int* cu = reinterpret_cast<int*>(smem + kThreads / 32);   // [B + 1] tokens before each request, cut at T
+  int* base = cu + a.B + 1;                       // [B + 1] free pages taken before each request
   const int tid = threadIdx.x;
   const bool first = blockIdx.x == 0;
   pdl_wait();
@@ -153,16 +153,18 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(PlanArgs a) {
   }
 }
 
+constexpr size_t plan_smem(int B) { return kThreads / 32 * sizeof(long long) + 2 * ((size_t)B + 1) * sizeof(int); }
+
 }  // namespace
 
 int chunk_plan_max_requests() { return kMaxReq; }
 
 cudaError_t launch_chunk_plan(const PlanArgs& a, cudaStream_t s) {
   const int grid = a.T > 0 ? (a.T + kTokens - 1) / kTokens : 1;
-  const size_t smem = 2 * (size_t)(a.B + 1) * sizeof(int);
-  if (smem > 48 * 1024) {
+  const size_t smem = plan_smem(a.B);
+  if (smem > 48 * 1024) {       // more than a kernel has without asking
     const cudaError_t e = cudaFuncSetAttribute(chunk_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               2 * (kMaxReq + 1) * (int)sizeof(int));
+                                               (int)plan_smem(kMaxReq));
     if (e != cudaSuccess) return e;
   }
   return launch_k(chunk_plan_kernel, dim3(grid), dim3(kThreads), smem, s, 1, a);

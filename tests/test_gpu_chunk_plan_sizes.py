@@ -1,4 +1,10 @@
-"""Block tables of steps at the ends of the range: idle steps without requests."""
+"""Block tables of steps at the ends of the range: idle steps without requests,
+and batches around the size where the kernel's shared memory has to be asked
+for."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -29,3 +35,26 @@ def test_an_idle_step_has_results_of_its_own(q, T, rows):
     for t in (req, pos, slot):
         assert bool((t == -1).all())
     assert bool((table == -5).all())
+
+
+SIZES = """
+import torch
+from indexer_top_sparse_c4_b200 import qsa
+i = lambda n, fill=-5: torch.full((n,), fill, dtype=torch.int32, device="cuda")
+for B in (6135, 6136, 6143, 6144, 8192):
+    cu, kv, taken, status = i(B + 1), i(B), i(1), i(1, 0)
+    req, pos, slot = i(B), i(B), i(B)
+    free = torch.arange(B, dtype=torch.int32, device="cuda")
+    qsa.qsa_chunk_plan(i(B, 0), i(B, 1), free, i(B).view(B, 1), B, cu, kv, req, pos, slot, taken, dev_status=status)
+    want = torch.arange(B, device="cuda")
+    assert int(status) == 0 and int(taken) == B and int(cu[B]) == B
+    assert torch.equal(req.long(), want) and torch.equal(slot.long(), want * 64) and bool((pos == 0).all())
+print("served")
+"""
+
+
+def test_every_batch_size_in_a_process_of_its_own(q):
+    """Sizes in ascending order, before any larger one has raised a limit."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", SIZES], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "served" in r.stdout, r.stderr[-2000:]
