@@ -460,8 +460,9 @@ QSA_API qsa_status_t qsa_chunk_plan(const int32_t* n_cached, const int32_t* n_ne
  * first sec0 frequencies take axis 0, the next sec1 axis 1, the last sec2 axis
  * 2; otherwise axis 1 has i % 3 == 1 below 3 sec1, axis 2 has i % 3 == 2 below
  * 3 sec2, and axis 0 the rest.  sec0 + sec1 + sec2 = rot_dim / 2; one axis:
- * (rot_dim / 2, 0, 0).  Angles are reduced in 64 bits, so far positions keep
- * their precision; the rotation is in FP32 and rounded once.
+ * (rot_dim / 2, 0, 0).  Angles are reduced to a fraction of a turn in pairs of
+ * 64-bit values, so every position has the precision of small ones; the
+ * rotation is in FP32 and rounded once.
  * q_out [T, Hq, D] in x_dt (it may be q itself when q is contiguous).  The
  * rotated keys and the values go to rows slot[t] of k_pages / v_pages (kv_dt
  * F32, BF16 or FP8_E4M3: code = value / scale to nearest even, values past 448

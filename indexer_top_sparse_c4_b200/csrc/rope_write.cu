@@ -12,10 +12,13 @@
 //   interleaved  1 where i % 3 == 1 and i < 3 sec1, 2 where i % 3 == 2 and
 //                i < 3 sec2, otherwise 0
 //
-// Angles: at position 262,144 a 32-bit product is off by up to 2^-7 radians, so
-// the product is formed in 64 bits (exact: 31 + 24 bits), divided by 2 pi and
-// reduced to a fraction of a turn there; sine and cosine of the fraction (at
-// most half a turn, in 32 bits) are then good to a few units of 2^-24.
+// Angles: at position 262,144 a 32-bit product is off by up to 2^-7 radians.  A
+// position of 31 bits times a frequency of 24 does not fit the 53 bits of a
+// double either, and 1 / (2 pi) is known to no finite number of them, so both
+// the product and the quotient are carried as two doubles (angle_turns): the
+// fraction of a turn is good to 2^-53 of a turn at every position, and what
+// remains is its rounding to FP32 and the sine's and cosine's own, a few units
+// of 2^-24 of each, small sines near whole turns included.
 //
 // Bound: HBM for a prefill chunk (each value is read and written once), the
 // launch for a decode step.  A warp takes a token, or with few tokens a part
@@ -65,6 +68,16 @@ __device__ __forceinline__ void store8(__nv_fp8_e4m3* p, const Vec8& x, float sc
     w[j] = (uint32_t)lo | ((uint32_t)hi << 16);
   }
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+// pos * freq / (2 pi) less the nearest whole turns, in -1/2 .. 1/2.
+__device__ __forceinline__ float angle_turns(int pos, float freq) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;   // 1 / (2 pi)
+  const double p = pos, f = freq;
+  const double a = __dmul_rn(p, f), a_lo = fma(p, f, -a);                      // p f, exactly
+  const double t = __dmul_rn(a, kHi);
+  const double t_lo = fma(a, kHi, -t) + fma(a, kLo, a_lo * kHi);
+  return (float)((t - rint(t)) + t_lo);
 }
 
 __device__ __forceinline__ int axis_of(const RopeArgs& a, int i) {
@@ -172,10 +185,8 @@ __global__ void __launch_bounds__(kThreads, 6) rope_write_kernel(RopeArgs a, int
   constexpr int NF = ADJ ? 4 : 8;
   const int fu = half / NF;
   for (int f = lane; f < half; f += 32) {
-    const double angle = (double)a.pos[(size_t)axis_of(a, f) * a.pos_stride + t] * (double)a.inv_freq[f];
-    const double turns = angle * 0.15915494309189533577;  // 1 / (2 pi)
     float s, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+    sincospif(2.f * angle_turns(a.pos[(size_t)axis_of(a, f) * a.pos_stride + t], a.inv_freq[f]), &s, &c);
     cs_smem[warp][(f % NF) * fu + f / NF] = make_float2(c * a.rot_scale, s * a.rot_scale);
   }
   __syncwarp();
