@@ -55,8 +55,9 @@ _binding = None   # a _Recorder while bind() runs a wrapper
 
 class _Recorder:
     """Stands in for the library while bind() runs a wrapper: the launching
-    calls are recorded with their converted arguments (and report QSA_OK),
-    everything else (size queries, names) goes to the library."""
+    calls are recorded with their converted arguments and the device current
+    then (and report QSA_OK), everything else (size queries, names) goes to the
+    library."""
 
     def __init__(self, real):
         self.real, self.calls = real, []
@@ -68,7 +69,10 @@ class _Recorder:
             return fn
 
         def record(*args):
-            self.calls.append((fn, args))
+            dev = _current_device() if torch.cuda.is_initialized() else None
+            if not self.calls or self.calls[-1][0] != dev:
+                self.calls.append((dev, []))
+            self.calls[-1][1].append((fn, args))
             return QSA_OK
         return record
 
@@ -76,11 +80,12 @@ class _Recorder:
 def bind(fn, *args, **kwargs):
     """The libqsa calls that ``fn(*args, **kwargs)`` makes, with their
     ctypes arguments built once: returns a zero-argument callable that only
-    crosses into C, for host-bound loops.  The tensors and the stream the
-    calls name are fixed at binding: they must stay allocated and in place
-    (bind again after replacing one), and ``stream=None`` means the stream
-    current now.  Bind from one thread at a time: while ``fn`` runs, lib()
-    hands out the recorder."""
+    crosses into C, for host-bound loops.  The tensors, the stream and the
+    device of the calls are fixed at binding: the tensors must stay allocated
+    and in place (bind again after replacing one), ``stream=None`` means the
+    stream current now, and each call runs on the device it was bound on,
+    whichever is current when it is called.  Bind from one thread at a time:
+    while ``fn`` runs, lib() hands out the recorder."""
     global _binding
     rec = _Recorder(lib())
     _binding = rec
@@ -88,11 +93,19 @@ def bind(fn, *args, **kwargs):
         fn(*args, **kwargs)
     finally:
         _binding = None
-    calls = tuple(rec.calls)
+    parts = tuple((dev, tuple(calls)) for dev, calls in rec.calls)
 
-    def call():
+    def run(calls):
         for f, a in calls:
             _check(f(*a))
+
+    def call():
+        for dev, calls in parts:
+            if dev is None or dev == _current_device():
+                run(calls)
+            else:
+                with torch.cuda.device(dev):
+                    run(calls)
     return call
 
 
