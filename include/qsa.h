@@ -433,6 +433,8 @@ QSA_API qsa_status_t qsa_dcp_merge_attn(const float* o_parts, const float* lse_p
  * batch).  The inputs are not changed: a caller drops the first n_taken pages
  * from its free list.  B = 0 is an idle step: cu_new[0] and n_taken[0] are 0,
  * the T rows get -1, and n_cached, n_new, kv_len and page_table may be NULL.
+ * Outputs that overlap the lengths or the free list are refused: a loop that
+ * keeps its lengths in place copies kv_len back behind the call.
  * Device checks: a negative length counts as 0; tokens past T are cut (cu_new
  * and kv_len count the tokens kept); tokens past the page table's row have
  * slot -1 (all three: QSA_DEV_ROW_RANGE); when the free list runs out, the

@@ -25,6 +25,9 @@ qsa_status_t cuda_status(cudaError_t e, const char* what) {
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  return a_bytes && b_bytes && (uintptr_t)a < (uintptr_t)b + b_bytes && (uintptr_t)b < (uintptr_t)a + a_bytes;
+}
 
 #define REQUIRE(cond, ...) \
   do {                     \
@@ -520,6 +523,15 @@ qsa_status_t qsa_chunk_plan(const int32_t* n_cached, const int32_t* n_new, int B
   REQUIRE(B == 0 || (n_cached && n_new && page_table && kv_len), "null pointer argument");
   REQUIRE(free_pages || n_free == 0, "free_pages is NULL with n_free = %d", n_free);
   REQUIRE(T == 0 || (q_req && q_pos && slot), "null pointer argument");
+  // every CTA reads all lengths, and the free list, while others write
+  const struct { const int32_t* p; size_t n; } in[] = {{n_cached, (size_t)B}, {n_new, (size_t)B},
+                                                       {free_pages, (size_t)n_free}},
+      out[] = {{cu_new, (size_t)B + 1}, {kv_len, (size_t)B}, {q_req, (size_t)T}, {q_pos, (size_t)T}, {slot, (size_t)T},
+               {n_taken, 1}, {page_table, (size_t)pt_rows * pt_stride}};
+  for (const auto& i : in)
+    for (const auto& o : out)
+      REQUIRE(!overlap(i.p, 4 * i.n, o.p, 4 * o.n),
+              "n_cached, n_new and free_pages must not overlap the outputs (kv_len may not be n_cached)");
   qsa::PlanArgs a{n_cached, n_new, B, free_pages, n_free, page_table, pt_rows, pt_stride, num_pages, cu_new, kv_len,
                   T, q_req, q_pos, slot, n_taken, dev_status};
   return cuda_status(qsa::launch_chunk_plan(a, (cudaStream_t)stream), "qsa_chunk_plan launch");

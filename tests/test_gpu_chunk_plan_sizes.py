@@ -37,6 +37,25 @@ def test_an_idle_step_has_results_of_its_own(q, T, rows):
     assert bool((table == -5).all())
 
 
+def test_buffers_side_by_side(q):
+    """All arrays slices of one buffer, each behind the other: nothing overlaps,
+    an exhausted free list of no pages inside another array neither."""
+    B, T = 3, 9
+    sizes = dict(old=B, new=B, table=B * 2, cu=B + 1, kv=B, req=T, pos=T, slot=T, taken=1)
+    buf, at, v = _ints(sum(sizes.values())), 0, {}
+    for name, n in sizes.items():
+        v[name] = buf[at:at + n]
+        at += n
+    v["old"].copy_(torch.tensor([3, 64, 0], dtype=torch.int32))
+    v["new"].copy_(torch.tensor([5, 0, 0], dtype=torch.int32))
+    table = v["table"].view(B, 2)
+    table[:, 0] = torch.arange(B, dtype=torch.int32, device="cuda")
+    q.qsa_chunk_plan(v["old"], v["new"], v["slot"][4:4], table, 8, v["cu"], v["kv"], v["req"], v["pos"], v["slot"],
+                     v["taken"])
+    assert v["cu"].tolist() == [0, 5, 5, 5] and v["kv"].tolist() == [8, 64, 0] and v["taken"].tolist() == [0]
+    assert v["pos"].tolist() == [3, 4, 5, 6, 7, -1, -1, -1, -1] == v["slot"].tolist()
+
+
 SIZES = """
 import torch
 from indexer_top_sparse_c4_b200 import qsa
