@@ -579,7 +579,13 @@ def _rows(dev, name, x, T, H, D):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
     if x.get_device() != dev:
         raise ValueError(f"{name} is on {x.device}, the call runs on cuda:{dev}")
-    return x.data_ptr(), (s0 if T > 1 else H * D)
+    return x.data_ptr(), (_stride(name, s0) if T > 1 else H * D)
+
+
+def _stride(name, s):
+    if s >= 1 << 31:     # the library's strides are 32-bit; ctypes would cut this one short
+        raise ValueError(f"the rows of {name} are {s} values apart, more than 2^31 - 1")
+    return s
 
 
 def _cache_shape(k_pages, v_pages, Hkv, D):
@@ -627,7 +633,7 @@ def qsa_rope_write(q, k, v, pos, inv_freq, slot, q_out, k_pages, v_pages, sectio
         raise ValueError(f"pos is on {pos.device}, the call runs on cuda:{dev}")
     freq_p, slot_p, out_p, k_p, v_p, st_p = _pointers(dev, inv_freq, slot, q_out, k_pages, v_pages, dev_status)
     _call(lib().qsa_rope_write, dev, stream, qp, qs, kp, ks, vp, vs, x_dt, pos.data_ptr(), axes,
-          pos.stride(0) if axes > 1 else T, *sec, 1 if interleaved_axes else 0, 1 if adjacent_pairs else 0, freq_p,
+          _stride("pos", pos.stride(0)) if axes > 1 else T, *sec, 1 if interleaved_axes else 0, 1 if adjacent_pairs else 0, freq_p,
           2 * half, float(rot_scale), slot_p, T, Hq, Hkv, D, out_p, k_p, v_p, kv_dt, float(k_scale), float(v_scale),
           num_pages, st_p)
     return q_out
