@@ -501,7 +501,8 @@ QSA_API qsa_status_t qsa_rope_write(const void* q, int q_stride, const void* k, 
  * FP8_E4M3 (value = code * scale); B <= 1,024; pt_stride <= 2^20.  A BF16 query on a BF16 or FP8
  * cache runs on the tensor cores: logits, softmax and sums in FP32, the
  * probabilities rounded to the type of the product with V (BF16 for a BF16
- * cache, FP16 for an FP8 cache).  Other pairs run in FP32.
+ * cache, FP16 for an FP8 cache, where one below 2^-21 of its row's largest is
+ * subnormal: off by up to 2^-32 of the largest).  Other pairs run in FP32.
  * The host sees the lengths' sum alone: T / B sets the height of the tiles, so
  * a T far above the tokens in use (heavy padding) or one long chunk among many
  * single tokens costs time, and another T may change results within those
