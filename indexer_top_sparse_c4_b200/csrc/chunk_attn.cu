@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
         *reinterpret_cast<float4*>(&sm.v[r][d]) = make_float4(y[0], y[1], y[2], y[3]);
       }
       __syncthreads();
-      // logits (base 2) of rows rg*4.., keys cg + 16 j
+      // logits (base 2) of rows rg * kR and the next, keys cg + 16 j
       float s[kR][4] = {};
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) chunk_simt_kernel(ChunkArgs a, Chunk
 // warps and joined in shared memory.  The order of the sums is fixed.
 constexpr int kCombineThreads = 256;
 // CTAs to a worker's tile.  Narrow tiles: 8, as most of a small step's only find
-// that nothing is shared (one request of 64 tokens: 9.5 us, 10.7 with 16); else
+// that nothing is shared (one token behind 63: 9.5 us, 10.7 with 16); else
 // 16 (8: float32 prompts 23 us instead of 20).
 constexpr int kCombineFew = 8, kCombineWide = 16;
 template <int D, typename OT>
@@ -341,11 +341,15 @@ cudaError_t launch_simt_kv(const ChunkArgs& a, const ChunkWs& ws, int grid, floa
 // 16 rows the narrow tiles read the cache once per 16.
 // Measured, 16/2 heads, narrow against wide (us):
 //   rows  batch         D 256 BF16  FP8        D 128 BF16  FP8
-//   8     8 x 65,000    164 : 218   91 : 211   88 : 168    56 : 189
-//   16    8 x 65,000    175 : 219   118 : 212  92 : 169    78 : 189
-//   24    8 x 65,000    330 : 221   199 : 214  165 : 169   137 : 189
-//   32    8 x 65,000    331 : 206   201 : 199  167 : 141   137 : 155
-//   32    64 x 300      43 : 31     44 : 37    29 : 26     29 : 29
+//   8     8 x 65,000    163 : 210   95 : 216   88 : 173    56 : 184
+//   16    8 x 65,000    180 : 212   126 : 214  93 : 167    80 : 183
+//   24    8 x 65,000    330 : 213   206 : 213  165 : 170   138 : 184
+//   32    8 x 65,000    332 : 198   218 : 205  167 : 147   150 : 160
+//   32    64 x 300      46 : 32     45 : 36    29 : 24     28 : 29
+// The average misses batches that are far from it: a T padded from 8 to 160
+// tokens puts 8 x 65,000 FP8 on the wide tiles (211 us instead of 92), and 64
+// tokens behind 3,000 beside a prompt of 2,000 take 248 us in one call, 59 + 110
+// in two (BF16: 128 against 74 + 54).
 int few_rows(const ChunkArgs& a) {
   const int G = a.Hq / a.Hkv;
   const int rows = (a.T + a.B - 1) / a.B * G;   // of an average request

@@ -21,6 +21,8 @@
 // GHz, copies issued under elect.sync and shorter softmax steps from 375 to 342.
 // BF16 at D 256: 165 us for 8 x 65,000 tokens, 0.98 of the copy rate.
 //
+//  * registers: up to 255 a thread; at 16 rows the D 256 forms spill (FP8 72 bytes
+//    stored, BF16 4), the others nothing.
 //  * every warp works on its own: it takes every W-th step of 16 keys of the
 //    CTA's piece, loads keys and values by TMA into its own ring (one lane
 //    issues, an mbarrier per slot, the next piece's first steps behind this
@@ -64,7 +66,7 @@ struct FewCfg {
   static constexpr int kSlot = kStep * D * E;            // a step's keys, or its values
   // Warps: four for BF16 at D 256 (six: 176 instead of 167 us for 8 x 65,000
   // tokens); twelve where a step's codes are few and its fixed part weighs
-  // (FP8 at D 128: 69 us, eight 81); else eight (twelve at D 256 FP8: 332 instead
+  // (FP8 at D 128: 56 us, eight 61); else eight (twelve at D 256 FP8: 332 instead
   // of 342 us for 8 x 262,144 tokens when power holds the clock down, but 48.4
   // instead of 46.7 for 64 x 3,000).
   static constexpr int W = kSlot >= 8192 ? 4 : FP8 && D <= 128 && NT == 1 ? 12 : 8;

@@ -54,12 +54,16 @@
 // 1,330 TFLOP/s, 0.97 of what cuBLAS sustains under the power limit; 1,467
 // TFLOP/s behind 24,576 tokens.  FP8 there: 1,267.  Bound by the tensor cores at
 // D 256 (2,130 cycles a tile when fed, measured); at D 128 and 64 (858 and 437
-// TFLOP/s) by the softmax: 128 x 128 exponentials take 1,024 cycles of the
-// 16-a-clock unit and the rest of the tile's chain about as long, which two
-// tiles in flight do not hide.  Two groups of warps that take whole tiles in
-// turn were 5 to 9% faster there and 5% slower at D 256.  Short items cost what
-// surrounds them: about 8 us from the launch to the first product (schedule,
-// page lookups, queries, first keys), 3 us for an item's output.
+// TFLOP/s, about 2,700 cycles a tile at both) by the chain of one tile's softmax:
+// wait, TMEM load, maximum, exchange, exponentials, TMEM store, which all warps
+// walk in step.  The 128 x 128 exponentials are 1,024 of those cycles, the
+// products 1,065 (D 128) or 530, so neither unit is full.  Two groups of warps
+// that take whole tiles in turn were 5 to 9% faster there and 5% slower at
+// D 256.  Short items cost what surrounds them: about 8 us from the launch to
+// the first product (schedule, page lookups, queries, first keys), 3 us for an
+// item's output.  The compiler spills in every form (BF16 272 to 316 bytes
+// stored, FP8 340 to 448): it allots the launch's 168 or 128 registers to all
+// roles, whatever setmaxnreg gives the softmax warps later.
 #include <cuda.h>
 
 #include "chunk_common.cuh"

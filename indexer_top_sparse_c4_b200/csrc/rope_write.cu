@@ -28,8 +28,10 @@
 // loads in flight.  Measured (8,192 tokens, 24/2 heads of D 256, BF16): 44 us,
 // 5.3 TB/s; one CTA per four tokens with the angles read from shared memory
 // for every head took 60 us (eight lanes to a bank), and four heads in flight
-// at twice the registers 57 us.  A rotated pair is read and written by the
-// same lane, so the queries may be rotated in place.
+// at twice the registers 57 us.  Six CTAs an SM allow 80 registers, for which
+// all forms but BF16 to F32 spill a little (BF16 to BF16 and FP8 24 bytes
+// stored, with adjacent pairs 4 and 28; F32 56 to 68).  A rotated pair is read
+// and written by the same lane, so the queries may be rotated in place.
 #include "qsa_internal.cuh"
 
 namespace qsa {
@@ -37,7 +39,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxHalf = 128;
-constexpr int kWarps = 4736;   // warps a call is spread over, if its heads are enough (32 per SM)
+constexpr int kWarps = 4736;   // warps a call is spread over, if its heads are enough (32 an SM; 24 are resident)
 
 struct Vec8 {
   float v[8];
@@ -237,8 +239,10 @@ __global__ void __launch_bounds__(kThreads, 6) rope_write_kernel(RopeArgs a, int
 template <bool ADJ, typename XT, typename KVT>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
   const int lg = a.D == 64 ? 2 : a.D == 128 ? 3 : 4;
-  // a warp per token, or, with few tokens, per part of a token's heads: a
-  // whole pass of the warp's groups at least, and as many warps as 148 SMs hold
+  // a warp per token, or, with few tokens, per part of a token's heads: a whole
+  // pass of the warp's groups at least, and up to about kWarps of them.  (A few
+  // thousand tokens are cut finer than they need to be: 2,360 of 28 heads make
+  // 7,080 warps, two rounds of the 3,552 that are resident.)
   const int heads = a.Hq + 2 * a.Hkv, groups = 32 >> lg;
   const int want = (kWarps + a.T - 1) / a.T;
   const int part_heads = (heads + want - 1) / want > groups ? ((heads + want - 1) / want + groups - 1) / groups * groups : groups;
