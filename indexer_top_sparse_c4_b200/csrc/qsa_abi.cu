@@ -602,7 +602,7 @@ qsa_status_t qsa_chunk_attn(const void* q, qsa_dtype_t q_dt, const void* k_pages
   SUPPORT(Hq / Hkv <= 16, "at most 16 query heads per KV head (got %d)", Hq / Hkv);
   SUPPORT(D == 64 || D == 128 || D == 256, "head dim D must be 64, 128 or 256 (got %d)", D);
   SUPPORT((long long)Hq * D <= (1 << 24), "too many heads (Hq=%d)", Hq);
-  REQUIRE(num_pages >= 1 && pt_rows >= 1 && pt_stride >= 1, "num_pages, pt_rows and pt_stride must be >= 1");
+  REQUIRE(num_pages >= 1 && pt_rows >= (B > 0) && pt_stride >= 1, "num_pages, pt_rows and pt_stride must be >= 1");
   SUPPORT(num_pages <= kMaxPages, "num_pages = %d exceeds %d", num_pages, kMaxPages);
   SUPPORT(pt_stride <= kMaxAttnPages, "pt_stride = %d exceeds %d", pt_stride, kMaxAttnPages);
   REQUIRE(B <= pt_rows, "B = %d requests need as many page-table rows (got %d)", B, pt_rows);
