@@ -527,7 +527,7 @@ qsa_status_t qsa_chunk_plan(const int32_t* n_cached, const int32_t* n_new, int B
   const struct { const int32_t* p; size_t n; } in[] = {{n_cached, (size_t)B}, {n_new, (size_t)B},
                                                        {free_pages, (size_t)n_free}},
       out[] = {{cu_new, (size_t)B + 1}, {kv_len, (size_t)B}, {q_req, (size_t)T}, {q_pos, (size_t)T}, {slot, (size_t)T},
-               {n_taken, 1}, {page_table, (size_t)pt_rows * pt_stride}};
+               {n_taken, 1}, {page_table, (size_t)B * pt_stride}};   // rows past B are not written
   for (const auto& i : in)
     for (const auto& o : out)
       REQUIRE(!overlap(i.p, 4 * i.n, o.p, 4 * o.n),

@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 B, T, N_FREE, ROWS, WIDTH = 5, 40, 12, 6, 8
-SIZES = dict(n_cached=B, n_new=B, free_pages=N_FREE, page_table=ROWS * WIDTH, cu_new=B + 1, kv_len=B, q_req=T, q_pos=T,
+SIZES = dict(n_cached=B, n_new=B, free_pages=N_FREE, page_table=B * WIDTH, cu_new=B + 1, kv_len=B, q_req=T, q_pos=T,
              slot=T, n_taken=1)
 INPUTS = ("n_cached", "n_new", "free_pages")
 

@@ -56,6 +56,17 @@ def test_buffers_side_by_side(q):
     assert v["pos"].tolist() == [3, 4, 5, 6, 7, -1, -1, -1, -1] == v["slot"].tolist()
 
 
+def test_a_free_list_in_a_spare_row_of_the_table(q):
+    """Rows past the batch's are not written and may hold anything."""
+    table = _ints(3, 8)
+    table[2] = torch.arange(10, 18, dtype=torch.int32, device="cuda")
+    cu, kv, taken, (req, pos, slot) = _ints(3), _ints(2), _ints(1), (_ints(70) for _ in range(3))
+    q.qsa_chunk_plan(_ints(2, fill=0), torch.tensor([64, 6], dtype=torch.int32, device="cuda"), table[2], table, 20, cu, kv,
+                     req, pos, slot, taken)
+    assert taken.tolist() == [2] and table[:2, 0].tolist() == [10, 11] and table[2].tolist() == list(range(10, 18))
+    assert slot.tolist() == list(range(640, 704)) + list(range(704, 710))
+
+
 SIZES = """
 import torch
 from indexer_top_sparse_c4_b200 import qsa
